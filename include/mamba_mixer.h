@@ -20,6 +20,11 @@
  *   mamba_ssd_state_update   Mamba-2 one-token step (decode), in place on the state
  *   mamba_m3_fwd             Mamba-3 prefill (trapezoid rule, complex state, 1/2/4 inputs per state)
  *   mamba_m3_state_update    Mamba-3 one-token step (decode), in place on the state
+ * the gated delta rule, whose update takes out what the state answers for the token's key:
+ *   mamba_gdr_fwd            prefill (chunked products on the tensor cores, or token by token)
+ *   mamba_gdr_state_update   one-token step (decode), in place on the state
+ * and a projection for a decoded token:
+ *   mamba_proj_q4            out = x W^T for a few rows of x, W in 4 bits with group scales
  *
  * and two status readers:
  *   mamba_check_status       did the last forward on this workspace complete? (per call)
@@ -583,6 +588,109 @@ mm_status mamba_m3_state_update(const void* x, const void* z, const void* dt, co
                                 const float* Dskip, float* state, const void* x_prev, const void* B_prev, void* y,
                                 int64_t batch, int64_t rank, int64_t heads, int64_t headdim, int64_t d_state,
                                 int64_t groups, void* stream);
+
+/*
+ * The gated delta rule, prefill: the Mamba-2 form's state and decay, with an
+ * update that first takes out what the state already answers for the token's
+ * key.  For value head h of H, key head g = h / (H / groups), state
+ * s [P = headdim, N = d_state] and every token t:
+ *
+ *   Delta_t = softplus(dt_t[h] + dt_bias[h]);  a_t = exp(Delta_t A[h]);  b_t = sigmoid(beta_t[h])
+ *   s_t     = a_t s_{t-1} + b_t (v_t[h] - a_t s_{t-1} k_t[g]) k_t[g]^T
+ *   y_t[h]  = scale s_t q_t[g]
+ *
+ * with q_t[g] and k_t[g] first divided by sqrt(sum of squares + norm_eps) when
+ * norm_eps > 0, and used as they are when it is 0 (the caller's keys then have
+ * |k|^2 <= 1 or so: b |k|^2 > 2 makes the recurrence itself grow).
+ *
+ *   q, k      [batch, seqlen, groups, d_state]   act   rows q_stride / k_stride elements apart
+ *   v         [batch, seqlen, heads, headdim]    act   rows v_stride elements apart
+ *   dt, beta  [batch, seqlen, heads]             act   before dt_bias and softplus; before the sigmoid
+ *   dt_bias   [heads] fp32 or NULL (= 0);  A [heads] fp32 (negative)
+ *   h0        [batch, heads, headdim, d_state]   fp32  or NULL (= 0)
+ *   y         [batch, seqlen, heads, headdim]    act   output
+ *   h_last    [batch, heads, headdim, d_state]   fp32  output: the state after the last token
+ *
+ * A row stride is the distance between a tensor's consecutive tokens in
+ * elements, at least its row's width and a multiple of 16 bytes; a sequence's
+ * first token follows the previous sequence's last at the same distance.  So
+ * q, k and v can be parts of one [batch, seqlen, q | k | v] tensor, as the
+ * layer's convolution writes it.
+ *
+ * Padding: a token with dt = -inf and beta = -inf (a = 1, b = 0) leaves the
+ * state as it is, whatever finite q, k and v it has; sequences of different
+ * lengths run as one batch that way (the padding's y is still written).
+ *
+ * bf16 calls of more than a few tokens run in chunks of 64 as dense products
+ * on the tensor cores, their operands in bf16 parts of 16 bits together, sums
+ * and the state in fp32; other calls run token by token in fp32.  Which one is
+ * a function of the sizes alone.
+ *
+ * Supported: d_state 64 or 128, headdim 64, 128, 192 or 256
+ * (MM_ERR_UNSUPPORTED otherwise); heads a multiple of groups, both positive,
+ * batch and heads <= 65535, seqlen <= 2^30 (MM_ERR_SHAPE).  norm_eps >= 0 and
+ * scale finite (MM_ERR_ARG).  Every pointer 16-byte aligned (MM_ERR_ALIGN); y
+ * and h_last may not overlap an input or each other (MM_ERR_ALIAS).
+ * workspace: at least mamba_gdr_workspace_size(...) bytes, 16-byte aligned,
+ * overlapping no other argument; its first 256 bytes hold the call's status
+ * for mamba_check_status.  seqlen == 0 writes h_last = h0 (or zeros).  Runs on
+ * `stream`; the library allocates nothing.  Errors otherwise as
+ * mamba_mixer_fwd.
+ */
+mm_status mamba_gdr_fwd(const void* q, const void* k, const void* v, const void* dt, const void* beta,
+                        const float* dt_bias, const float* A, const float* h0, void* y, float* h_last,
+                        int64_t batch, int64_t seqlen, int64_t groups, int64_t heads, int64_t headdim, int64_t d_state,
+                        int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale, float norm_eps,
+                        mm_dtype act, void* workspace, size_t workspace_bytes, void* stream);
+/* Workspace bytes of mamba_gdr_fwd for these sizes (0 if not supported): the
+ * status header and, where the call runs in chunks, each chunk's factors. */
+size_t mamba_gdr_workspace_size(int64_t batch, int64_t seqlen, int64_t heads, int64_t headdim, int64_t d_state,
+                                int64_t groups, mm_dtype act);
+
+/*
+ * One token of the gated delta rule (decode), in place on the state: the
+ * recurrence of mamba_gdr_fwd above for a single token, with the state the
+ * previous call (prefill or decode) left.
+ *
+ *   q, k      [batch, groups, d_state]           act   rows q_stride / k_stride elements apart
+ *   v         [batch, heads, headdim]            act   rows v_stride elements apart
+ *   dt, beta  [batch, heads]                     act
+ *   dt_bias   [heads] fp32 or NULL;  A [heads] fp32 (negative)
+ *   state     [batch, heads, headdim, d_state]   fp32  read and overwritten
+ *   y         [batch, heads, headdim]            act   output
+ *
+ * Supported sizes and errors as mamba_gdr_fwd (no workspace, no wait); state
+ * and y may not overlap an input or each other (MM_ERR_ALIAS).  One launch on
+ * `stream`; batch == 0 is a no-op.
+ */
+mm_status mamba_gdr_state_update(const void* q, const void* k, const void* v, const void* dt, const void* beta,
+                                 const float* dt_bias, const float* A, float* state, void* y,
+                                 int64_t batch, int64_t groups, int64_t heads, int64_t headdim, int64_t d_state,
+                                 int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale, float norm_eps,
+                                 mm_dtype act, void* stream);
+
+/*
+ * Projection of a few rows (the tokens of one decode step) by a weight of
+ * 4-bit numbers with group scales:
+ *
+ *   out[m, n] = sum_k x[m, k] s[n, k / group] (c[n, k] - z[n, k / group])
+ *
+ *   x       [M, K]          bf16, row-major
+ *   W       [N, K / 2]      bytes: c[n, 2i] in the low four bits of W[n, i], c[n, 2i + 1] in the high four; 0..15
+ *   scales  [N, K / group]  bf16
+ *   zeros   [N, K / group]  bf16, or NULL (= 8)
+ *   out     [M, N]          fp32 (out_dtype MM_F32) or bf16 (MM_BF16, rounded to nearest even)
+ *
+ * Sums are fp32; c - 8 and x enter the products exactly and each group's sum
+ * is scaled.  group is 32, 64 or 128 (MM_ERR_UNSUPPORTED otherwise) and
+ * divides K (MM_ERR_SHAPE); M <= 64 * 65535, N and K below 2^31.  Any M runs;
+ * the weight is read once per 64 rows, so mamba_proj_matmul suits a long
+ * prompt better.  Every pointer 16-byte aligned (MM_ERR_ALIGN); out may not
+ * overlap an input (MM_ERR_ALIAS).  No workspace; M == 0 is a no-op.  A wait
+ * that gives up is reported by mamba_mixer_fault_status.
+ */
+mm_status mamba_proj_q4(const void* x, const void* W, const void* scales, const void* zeros, void* out,
+                        int64_t M, int64_t N, int64_t K, int64_t group, mm_dtype out_dtype, void* stream);
 
 /* A static, human-readable name for a status code. */
 const char* mamba_status_string(mm_status status);

@@ -17,7 +17,8 @@ __all__ = [
     "MM_F32", "MM_BF16", "MixerError", "lib", "library_path", "mixer_fwd", "mixer_fwd_noalloc", "mixer_fwd_host",
     "state_update", "workspace_size", "host_workspace_size", "status_string", "abi_version", "fault_status",
     "check_status", "proj_matmul", "proj_matmul_workspace_size", "mixer_fwd_projected",
-    "projected_workspace_size", "ssd_fwd", "ssd_workspace_size", "ssd_state_update", "m3_fwd", "m3_state_update", "m3_workspace_size", "EXPORTED_SYMBOLS",
+    "projected_workspace_size", "ssd_fwd", "ssd_workspace_size", "ssd_state_update", "m3_fwd", "m3_state_update", "m3_workspace_size",
+    "gdr_fwd", "gdr_state_update", "gdr_workspace_size", "proj_q4", "EXPORTED_SYMBOLS",
 ]
 
 MM_F32 = 0
@@ -51,6 +52,10 @@ EXPORTED_SYMBOLS = (
     "mamba_m3_fwd",
     "mamba_m3_workspace_size",
     "mamba_m3_state_update",
+    "mamba_gdr_fwd",
+    "mamba_gdr_workspace_size",
+    "mamba_gdr_state_update",
+    "mamba_proj_q4",
 )
 
 
@@ -123,6 +128,14 @@ def _declare(L):
     L.mamba_m3_workspace_size.argtypes = [I64] * 7
     L.mamba_m3_state_update.restype = ctypes.c_int
     L.mamba_m3_state_update.argtypes = [P] * 14 + [I64] * 6 + [P]
+    L.mamba_gdr_fwd.restype = ctypes.c_int
+    L.mamba_gdr_fwd.argtypes = [P] * 10 + [I64] * 9 + [ctypes.c_float] * 2 + [ctypes.c_int, P, ctypes.c_size_t, P]
+    L.mamba_gdr_workspace_size.restype = ctypes.c_size_t
+    L.mamba_gdr_workspace_size.argtypes = [I64] * 6 + [ctypes.c_int]
+    L.mamba_gdr_state_update.restype = ctypes.c_int
+    L.mamba_gdr_state_update.argtypes = [P] * 9 + [I64] * 8 + [ctypes.c_float] * 2 + [ctypes.c_int, P]
+    L.mamba_proj_q4.restype = ctypes.c_int
+    L.mamba_proj_q4.argtypes = [P] * 5 + [I64] * 4 + [ctypes.c_int, P]
     return L
 
 
@@ -763,3 +776,154 @@ def m3_state_update(x, z, dt, trap, dt_bias, A, theta, Bm, Cm, Dskip, state, x_p
     _keep_alive_on(made, (stream,))
     return y
 
+
+def _check_rows(t, name, dtype, shape, device):
+    """A tensor [B, L, heads, width] (or [B, heads, width]) whose tokens' rows
+    are dense and evenly spaced, as a part of a wider packed tensor is.
+    Returns the elements between rows."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    heads, width = shape[-2:]
+    if (width > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != width):
+        raise ValueError(f"{name} must have contiguous rows of {heads} x {width}")
+    lead = [(n, s) for n, s in zip(shape[:-2], t.stride()[:-2])]
+    if any(n == 0 for n, _ in lead):
+        return heads * width
+    stride, rows = None, 1
+    for n, s in reversed(lead):
+        if n > 1:
+            if stride is None:
+                stride = s
+            elif s != rows * stride:
+                raise ValueError(f"{name} must have its tokens' rows evenly spaced")
+            rows *= n
+    return heads * width if stride is None else stride
+
+
+def gdr_workspace_size(batch, seqlen, heads, headdim=128, d_state=128, groups=1, act=MM_BF16) -> int:
+    return int(lib().mamba_gdr_workspace_size(batch, seqlen, heads, headdim, d_state, groups, act))
+
+
+def gdr_fwd(q, k, v, dt, beta, dt_bias, A, h0=None, *, scale=None, norm_eps=1e-6, y=None, h_last=None,
+            workspace=None, stream=None):
+    """The gated delta rule (mamba_gdr_fwd): q, k [B,L,G,N] and v [B,L,H,P]
+    (bf16 or fp32; they may be parts of one packed tensor, rows evenly spaced
+    and 16-byte multiples apart), dt and beta [B,L,H] (same dtype), dt_bias/A
+    [H] fp32 (dt_bias may be None), h0 [B,H,P,N] fp32 or None.  scale defaults
+    to N ** -0.5; q and k are L2-normalised with norm_eps, or used as they are
+    when it is 0.  Returns (y [B,L,H,P], h_last [B,H,P,N] fp32), allocating any
+    output not given."""
+    import torch
+
+    f32 = torch.float32
+    act = _act_code(v.dtype)
+    Bsz, L, H, P = v.shape
+    G, N = q.shape[2], q.shape[3]
+    dev = v.device
+    made = []
+    qs = _check_rows(q, "q", v.dtype, (Bsz, L, G, N), dev)
+    ks = _check_rows(k, "k", v.dtype, (Bsz, L, G, N), dev)
+    vs = _check_rows(v, "v", v.dtype, (Bsz, L, H, P), dev)
+    _check(dt, "dt", v.dtype, (Bsz, L, H), dev)
+    _check(beta, "beta", v.dtype, (Bsz, L, H), dev)
+    _check(dt_bias, "dt_bias", f32, (H,), dev)
+    _check(A, "A", f32, (H,), dev)
+    _check(h0, "h0", f32, (Bsz, H, P, N), dev)
+    if y is None:
+        y = torch.empty((Bsz, L, H, P), dtype=v.dtype, device=dev)
+        made.append(y)
+    if h_last is None:
+        h_last = torch.empty((Bsz, H, P, N), dtype=f32, device=dev)
+        made.append(h_last)
+    _check(y, "y", v.dtype, (Bsz, L, H, P), dev)
+    _check(h_last, "h_last", f32, (Bsz, H, P, N), dev)
+    with torch.cuda.device(dev):
+        ws_bytes = gdr_workspace_size(Bsz, L, H, P, N, G, act)
+        if workspace is None or workspace.numel() * workspace.element_size() < ws_bytes:
+            workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=dev)
+            made.append(workspace)
+        st = lib().mamba_gdr_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(dt_bias), _ptr(A), _ptr(h0),
+                                 _ptr(y), _ptr(h_last), Bsz, L, G, H, P, N, qs, ks, vs,
+                                 float(N ** -0.5 if scale is None else scale), float(norm_eps), act, _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if st != 0:
+        raise MixerError(st, "mamba_gdr_fwd")
+    _keep_alive_on(made, (stream,))
+    return y, h_last
+
+
+def gdr_state_update(q, k, v, dt, beta, dt_bias, A, state, *, scale=None, norm_eps=1e-6, y=None, stream=None):
+    """One token of the gated delta rule (mamba_gdr_state_update), in place on
+    state [B,H,P,N] fp32: q, k [B,G,N] and v [B,H,P] (bf16 or fp32; rows evenly
+    spaced), dt and beta [B,H], dt_bias/A [H] fp32 (dt_bias may be None).  scale
+    and norm_eps as gdr_fwd.  Returns y [B,H,P], allocated if not given."""
+    import torch
+
+    f32 = torch.float32
+    act = _act_code(v.dtype)
+    Bsz, H, P = v.shape
+    G, N = q.shape[1], q.shape[2]
+    dev = v.device
+    made = []
+    qs = _check_rows(q, "q", v.dtype, (Bsz, G, N), dev)
+    ks = _check_rows(k, "k", v.dtype, (Bsz, G, N), dev)
+    vs = _check_rows(v, "v", v.dtype, (Bsz, H, P), dev)
+    _check(dt, "dt", v.dtype, (Bsz, H), dev)
+    _check(beta, "beta", v.dtype, (Bsz, H), dev)
+    _check(dt_bias, "dt_bias", f32, (H,), dev)
+    _check(A, "A", f32, (H,), dev)
+    _check(state, "state", f32, (Bsz, H, P, N), dev)
+    if state is None:
+        raise ValueError("state must be given")
+    if y is None:
+        y = torch.empty((Bsz, H, P), dtype=v.dtype, device=dev)
+        made.append(y)
+    _check(y, "y", v.dtype, (Bsz, H, P), dev)
+    with torch.cuda.device(dev):
+        st = lib().mamba_gdr_state_update(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(dt_bias), _ptr(A),
+                                          _ptr(state), _ptr(y), Bsz, G, H, P, N, qs, ks, vs,
+                                          float(N ** -0.5 if scale is None else scale), float(norm_eps), act,
+                                          _stream_handle(stream))
+    if st != 0:
+        raise MixerError(st, "mamba_gdr_state_update")
+    _keep_alive_on(made, (stream,))
+    return y
+
+
+def proj_q4(x, W, scales, zeros=None, *, group=128, out=None, out_dtype=None, stream=None):
+    """out = x W^T for a few rows x [M,K] bf16 and a weight of 4-bit numbers
+    (mamba_proj_q4): W [N,K/2] uint8 (even inputs in the low four bits), scales
+    and zeros [N,K/group] bf16 (zeros None: 8), weight = scale (number - zero).
+    out [M,N] fp32 (default) or bf16, allocated if not given."""
+    import torch
+
+    bf = torch.bfloat16
+    M, K = x.shape
+    N = W.shape[0]
+    dev = x.device
+    if group <= 0:
+        raise ValueError(f"group must be positive, got {group}")
+    _check(x, "x", bf, (M, K), dev)
+    _check(W, "W", torch.uint8, (N, K // 2), dev)
+    _check(scales, "scales", bf, (N, K // group), dev)
+    _check(zeros, "zeros", bf, (N, K // group), dev)
+    made = []
+    dtype = out_dtype or (out.dtype if out is not None else torch.float32)
+    code = _act_code(dtype)
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=dev)
+        made.append(out)
+    _check(out, "out", dtype, (M, N), dev)
+    with torch.cuda.device(dev):
+        st = lib().mamba_proj_q4(_ptr(x), _ptr(W), _ptr(scales), _ptr(zeros), _ptr(out), M, N, K, group, code,
+                                 _stream_handle(stream))
+    if st != 0:
+        raise MixerError(st, "mamba_proj_q4")
+    _keep_alive_on(made, (stream,))
+    return out

@@ -20,6 +20,8 @@
 #include "proj_ops.cuh"
 #include "ssd.cuh"
 #include "m3.cuh"
+#include "gdr.cuh"
+#include "proj_q4.cuh"
 
 namespace {
 
@@ -1843,6 +1845,271 @@ mm_status mamba_m3_state_update(const void* x, const void* z, const void* dt, co
     else if (rank == 2) mm::m3_state_update_kernel<2><<<grid, mm::kM3DecThreads, smem, s>>>(p);
     else mm::m3_state_update_kernel<4><<<grid, mm::kM3DecThreads, smem, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? MM_OK : MM_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- gated delta rule
+namespace {
+
+// One call of the gated delta rule, checked.  Row strides are in elements.
+struct GdrArgs {
+    const void *q, *k, *v, *dt, *beta;
+    const float *dt_bias, *A, *h0;
+    void* y;
+    float* h_last;
+    int64_t batch, seqlen, groups, heads, headdim, d_state, q_stride, k_stride, v_stride;
+    float scale, norm_eps;
+    mm_dtype act;
+};
+
+// Sizes the kernels address: grid limits, and element counts that stay far
+// inside 64 bits (a tensor's bytes below 2^48).
+bool gdr_sizes_ok(int64_t batch, int64_t seqlen, int64_t groups, int64_t heads) {
+    if (batch < 0 || seqlen < 0 || groups <= 0 || heads <= 0 || heads % groups != 0) return false;
+    if (batch > 65535 || heads > 65535 || seqlen > kMaxSeqlen) return false;
+    return batch * seqlen < (int64_t(1) << 36) && batch * seqlen * heads < (int64_t(1) << 38);
+}
+bool gdr_supported(int64_t headdim, int64_t d_state) {
+    return (d_state == 64 || d_state == 128) && headdim > 0 && headdim <= 256 && headdim % 64 == 0;
+}
+
+mm_status validate_gdr(const GdrArgs& a, bool in_place, Span* ins, Span* outs) {
+    if (a.act != MM_F32 && a.act != MM_BF16) return MM_ERR_DTYPE;
+    if (!gdr_sizes_ok(a.batch, a.seqlen, a.groups, a.heads)) return MM_ERR_SHAPE;
+    if (!gdr_supported(a.headdim, a.d_state)) return MM_ERR_UNSUPPORTED;
+    const int64_t es = a.act == MM_F32 ? 4 : 2, qw = a.groups * a.d_state, vw = a.heads * a.headdim;
+    const int64_t most = int64_t(1) << 32;     // elements between tokens
+    if (a.q_stride < qw || a.k_stride < qw || a.v_stride < vw || a.q_stride > most || a.k_stride > most || a.v_stride > most)
+        return MM_ERR_SHAPE;
+    if (!(a.norm_eps >= 0.0f && a.norm_eps <= 3.402823466e38f) || !(a.scale >= -3.402823466e38f && a.scale <= 3.402823466e38f))
+        return MM_ERR_ARG;
+    if (a.batch == 0) return MM_OK;
+    const int64_t tokens = a.batch * a.seqlen;
+    if (!a.A || !a.h_last || (in_place && !a.h0) || (tokens > 0 && (!a.q || !a.k || !a.v || !a.dt || !a.beta || !a.y)))
+        return MM_ERR_NULL;
+    for (const void* q : {a.q, a.k, a.v, a.dt, a.beta, static_cast<const void*>(a.dt_bias), static_cast<const void*>(a.A),
+                          static_cast<const void*>(a.h0), static_cast<const void*>(a.y), static_cast<const void*>(a.h_last)})
+        if (q && !aligned16(q)) return MM_ERR_ALIGN;
+    if (a.q_stride * es % 16 != 0 || a.k_stride * es % 16 != 0 || a.v_stride * es % 16 != 0) return MM_ERR_ALIGN;
+    // a strided tensor spans from its first row to the end of its last
+    auto rows = [&](const void* p, int64_t stride, int64_t width) {
+        return span(p, tokens > 0 ? ((tokens - 1) * stride + width) * es : 0);
+    };
+    const int64_t states = a.batch * a.heads * a.headdim * a.d_state * 4;
+    ins[0] = rows(a.q, a.q_stride, qw);
+    ins[1] = rows(a.k, a.k_stride, qw);
+    ins[2] = rows(a.v, a.v_stride, vw);
+    ins[3] = span(a.dt, tokens * a.heads * es);
+    ins[4] = span(a.beta, tokens * a.heads * es);
+    ins[5] = span(a.dt_bias, a.heads * 4);
+    ins[6] = span(a.A, a.heads * 4);
+    ins[7] = span(in_place ? nullptr : a.h0, states);
+    outs[0] = span(a.y, tokens * vw * es);
+    outs[1] = span(a.h_last, states);
+    for (int i = 0; i < 8; ++i)
+        if (overlaps(outs[0], ins[i]) || overlaps(outs[1], ins[i])) return MM_ERR_ALIAS;
+    return overlaps(outs[0], outs[1]) ? MM_ERR_ALIAS : MM_OK;
+}
+
+mm::GdrParams gdr_params(const GdrArgs& a) {
+    mm::GdrParams p{};
+    p.q = a.q;
+    p.k = a.k;
+    p.v = a.v;
+    p.dt = a.dt;
+    p.beta = a.beta;
+    p.dt_bias = a.dt_bias;
+    p.A = a.A;
+    p.h0 = a.h0;
+    p.y = a.y;
+    p.h_last = a.h_last;
+    p.L = a.seqlen;
+    p.q_stride = a.q_stride;
+    p.k_stride = a.k_stride;
+    p.v_stride = a.v_stride;
+    p.H = static_cast<int>(a.heads);
+    p.G = static_cast<int>(a.groups);
+    p.P = static_cast<int>(a.headdim);
+    p.scale = a.scale;
+    p.eps = a.norm_eps;
+    return p;
+}
+
+template <typename T, int N, int RPT>
+cudaError_t launch_gdr_recurrent_t(const mm::GdrParams& p, int64_t batch, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(p.H * (p.P / (mm::kGdrRecThreads / 8 * RPT))), static_cast<unsigned>(batch));
+    mm::gdr_recurrent_kernel<T, N, RPT><<<grid, mm::kGdrRecThreads, forced_launch_failure() ? (1 << 20) : 0, s>>>(p);
+    return cudaGetLastError();
+}
+// State rows per lane: four once the grid fills the SMs with them (fewer
+// reads of q and k per row), one below that (the latency of a row decides).
+template <typename T, int N>
+cudaError_t launch_gdr_recurrent_n(const mm::GdrParams& p, int64_t batch, cudaStream_t s) {
+    const bool wide = batch * p.H * p.P / (mm::kGdrRecThreads / 8 * 4) >= 4 * plan_sms();
+    return wide ? launch_gdr_recurrent_t<T, N, 4>(p, batch, s) : launch_gdr_recurrent_t<T, N, 1>(p, batch, s);
+}
+mm_status launch_gdr_recurrent(const mm::GdrParams& p, const GdrArgs& a, cudaStream_t s) {
+    cudaError_t e;
+    if (a.act == MM_F32)
+        e = a.d_state == 64 ? launch_gdr_recurrent_n<float, 64>(p, a.batch, s) : launch_gdr_recurrent_n<float, 128>(p, a.batch, s);
+    else
+        e = a.d_state == 64 ? launch_gdr_recurrent_n<__nv_bfloat16, 64>(p, a.batch, s)
+                            : launch_gdr_recurrent_n<__nv_bfloat16, 128>(p, a.batch, s);
+    return e == cudaSuccess ? MM_OK : MM_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mamba_gdr_workspace_size(int64_t batch, int64_t seqlen, int64_t heads, int64_t headdim, int64_t d_state,
+                                int64_t groups, mm_dtype act) {
+    if ((act != MM_F32 && act != MM_BF16) || batch <= 0 || !gdr_sizes_ok(batch, seqlen, groups, heads) ||
+        !gdr_supported(headdim, d_state))
+        return 0;
+    return kWsHeader;
+}
+
+mm_status mamba_gdr_fwd(const void* q, const void* k, const void* v, const void* dt, const void* beta,
+                        const float* dt_bias, const float* A, const float* h0, void* y, float* h_last,
+                        int64_t batch, int64_t seqlen, int64_t groups, int64_t heads, int64_t headdim, int64_t d_state,
+                        int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale, float norm_eps,
+                        mm_dtype act, void* workspace, size_t workspace_bytes, void* stream)
+{
+    const GdrArgs a{q, k, v, dt, beta, dt_bias, A, h0, y, h_last, batch, seqlen, groups, heads, headdim, d_state,
+                    q_stride, k_stride, v_stride, scale, norm_eps, act};
+    Span ins[8], outs[2];
+    if (mm_status st = validate_gdr(a, false, ins, outs); st != MM_OK) return st;
+    if (batch == 0) return MM_OK;
+    const size_t need = mamba_gdr_workspace_size(batch, seqlen, heads, headdim, d_state, groups, act);
+    if (!workspace || workspace_bytes < need) return MM_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MM_ERR_ALIGN;
+    const Span sw = span(workspace, static_cast<int64_t>(need));
+    for (const Span& in : ins)
+        if (overlaps(sw, in)) return MM_ERR_ALIAS;
+    if (overlaps(sw, outs[0]) || overlaps(sw, outs[1])) return MM_ERR_ALIAS;
+    if (mm_status st = check_device(); st != MM_OK) return st;
+    mm::GdrParams p = gdr_params(a);
+    p.status = static_cast<unsigned long long*>(workspace);
+    p.status_epoch = next_call_id();
+    return launch_gdr_recurrent(p, a, static_cast<cudaStream_t>(stream));
+}
+
+mm_status mamba_gdr_state_update(const void* q, const void* k, const void* v, const void* dt, const void* beta,
+                                 const float* dt_bias, const float* A, float* state, void* y,
+                                 int64_t batch, int64_t groups, int64_t heads, int64_t headdim, int64_t d_state,
+                                 int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale, float norm_eps,
+                                 mm_dtype act, void* stream)
+{
+    const GdrArgs a{q, k, v, dt, beta, dt_bias, A, state, y, state, batch, 1, groups, heads, headdim, d_state,
+                    q_stride, k_stride, v_stride, scale, norm_eps, act};
+    Span ins[8], outs[2];
+    if (mm_status st = validate_gdr(a, true, ins, outs); st != MM_OK) return st;
+    if (batch == 0) return MM_OK;
+    if (mm_status st = check_device(); st != MM_OK) return st;
+    return launch_gdr_recurrent(gdr_params(a), a, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- projection with 4-bit weights
+namespace {
+
+// 2-D map over rows of `cols` elements in 128-byte boxes with the 128-byte
+// swizzle: packed weights (bytes) or bf16.
+bool encode_q4_2d(CUtensorMap* m, const void* base, bool bytes, int64_t cols, int64_t rows, int box_rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int64_t es = bytes ? 1 : 2;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * es)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int GB, int MT, bool ZEROS, bool OUT_BF16>
+cudaError_t launch_q4_t(mm::Q4Params p, const void* x, const void* W, cudaStream_t s) {
+    CUtensorMap tw, tx;
+    if (!encode_q4_2d(&tw, W, true, p.K / 2, p.N, mm::kQ4Rows) || !encode_q4_2d(&tx, x, false, p.K, p.M, MT * 8))
+        return cudaErrorInvalidValue;
+    auto kern = mm::proj_q4_kernel<GB, MT, ZEROS, OUT_BF16>;
+    static std::atomic<unsigned long long> smem_allowed{0};
+    if (cudaError_t e = allow_smem(kern, smem_allowed); e != cudaSuccess) return e;
+    // K is split over a cluster until the grid covers the SMs or a CTA has two slots
+    const int64_t tiles = (static_cast<int64_t>(p.N) + mm::kQ4Rows - 1) / mm::kQ4Rows * ((p.M + MT * 8 - 1) / (MT * 8));
+    const int slots = (p.K + mm::kQ4K - 1) / mm::kQ4K;
+    int split = 1;
+    while (split < 8 && tiles * split < plan_sms() && slots >= 4 * split) split *= 2;
+    p.slots_per_cta = (slots + split - 1) / split;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((p.N + mm::kQ4Rows - 1) / mm::kQ4Rows),
+                       static_cast<unsigned>((p.M + MT * 8 - 1) / (MT * 8)), static_cast<unsigned>(split));
+    cfg.blockDim = dim3(mm::kQ4Threads);
+    cfg.dynamicSmemBytes = forced_launch_failure() ? size_t(1) << 20 : static_cast<size_t>(mm::Q4Layout<MT>::smem_bytes);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = static_cast<unsigned>(split);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, tw, tx);
+}
+template <int GB, int MT>
+cudaError_t launch_q4_m(const mm::Q4Params& p, const void* x, const void* W, bool bf16, cudaStream_t s) {
+    if (p.zeros) return bf16 ? launch_q4_t<GB, MT, true, true>(p, x, W, s) : launch_q4_t<GB, MT, true, false>(p, x, W, s);
+    return bf16 ? launch_q4_t<GB, MT, false, true>(p, x, W, s) : launch_q4_t<GB, MT, false, false>(p, x, W, s);
+}
+// Tiles of eight rows of x per CTA: as few as hold them all, up to 64 rows
+// (above that, the weight is read once per 64 rows).
+template <int GB>
+cudaError_t launch_q4_g(const mm::Q4Params& p, const void* x, const void* W, bool bf16, cudaStream_t s) {
+    if (p.M <= 8) return launch_q4_m<GB, 1>(p, x, W, bf16, s);
+    if (p.M <= 16) return launch_q4_m<GB, 2>(p, x, W, bf16, s);
+    if (p.M <= 32) return launch_q4_m<GB, 4>(p, x, W, bf16, s);
+    return launch_q4_m<GB, 8>(p, x, W, bf16, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+mm_status mamba_proj_q4(const void* x, const void* W, const void* scales, const void* zeros, void* out,
+                        int64_t M, int64_t N, int64_t K, int64_t group, mm_dtype out_dtype, void* stream)
+{
+    if (out_dtype != MM_F32 && out_dtype != MM_BF16) return MM_ERR_DTYPE;
+    if (M < 0 || N <= 0 || K <= 0 || M > int64_t(65535) * 64 || N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31))
+        return MM_ERR_SHAPE;
+    if (group != 32 && group != 64 && group != 128) return MM_ERR_UNSUPPORTED;
+    if (K % group != 0) return MM_ERR_SHAPE;
+    if (M == 0) return MM_OK;
+    if (!x || !W || !scales || !out) return MM_ERR_NULL;
+    for (const void* q : {x, W, scales, zeros, static_cast<const void*>(out)})
+        if (q && !aligned16(q)) return MM_ERR_ALIGN;
+    const Span so = span(out, M * N * (out_dtype == MM_F32 ? 4 : 2));
+    if (overlaps(so, span(x, M * K * 2)) || overlaps(so, span(W, N * (K / 2))) ||
+        overlaps(so, span(scales, N * (K / group) * 2)) || overlaps(so, span(zeros, N * (K / group) * 2)))
+        return MM_ERR_ALIAS;
+    if (mm_status st = check_device(); st != MM_OK) return st;
+    mm::Q4Params p{};
+    p.scales = static_cast<const __nv_bfloat16*>(scales);
+    p.zeros = static_cast<const __nv_bfloat16*>(zeros);
+    p.out = out;
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.K = static_cast<int>(K);
+    p.wait_limit = copy_wait_limit();
+    const bool bf16 = out_dtype == MM_BF16;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = group == 32 ? launch_q4_g<1>(p, x, W, bf16, s)
+                        : group == 64 ? launch_q4_g<2>(p, x, W, bf16, s) : launch_q4_g<4>(p, x, W, bf16, s);
+    if (e != cudaSuccess) { cudaGetLastError(); return MM_ERR_CUDA; }
+    return MM_OK;
 }
 
 }  // extern "C"
