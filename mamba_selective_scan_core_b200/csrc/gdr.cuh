@@ -10,7 +10,9 @@
 // normalises them.
 //
 // gdr_recurrent_kernel runs that as it stands, token by token: the one-token
-// step (decode), short calls and fp32 activations.
+// step (decode), short calls and fp32 activations.  gdr_prep_kernel and
+// gdr_scan_kernel run longer bf16 calls in chunks of 64 tokens on the tensor
+// cores.
 #pragma once
 
 #include <cstdint>
@@ -182,6 +184,700 @@ gdr_recurrent_kernel(const GdrParams p)
 #pragma unroll
         for (int m = 0; m < M; ++m)
             *reinterpret_cast<float4*>(p.h_last + (srow + 4 * r) * N + 4 * e + 32 * m) = s[r][m];
+}
+
+// ---------------------------------------------------------------- in chunks
+// C = 64 tokens at a time.  With cum_i the chunk's inclusive prefix sum of
+// Delta A, e_ij = exp(cum_i - cum_j), k and q normalised and S the state
+// entering the chunk, the values a token really writes, u_i, solve
+//
+//     (I + L) u = diag(b) (v - diag(exp cum) k S^T),   L_ij = b_i (k_i . k_j) e_ij  for j < i
+//
+// so with T = (I + L)^-1 diag(b) and M_ij = scale (q_i . k_j) e_ij (j <= i)
+//
+//     X = v - diag(exp cum) k S^T            u = T X
+//     y = scale diag(exp cum) q S^T + (M T) X
+//     S <- exp(cum_C) S + u^T diag(exp(cum_C - cum)) k
+//
+// gdr_prep_kernel (chunk, head, batch), all chunks at once: the rows [T; M T]
+// and each token's factors, into the workspace.  gdr_scan_kernel (64 state
+// rows, head, batch), the chunks in order: three tcgen05 products a chunk,
+//
+//     1. [k; q] S^T       128 x 64 x N     k and q as they arrive (bf16, exact)
+//     2. [T; M T] X       128 x 64 x 64
+//     3. k^T u'           N x 64 x 64      u' = diag(exp(cum_C - cum)) u
+//
+// with k's and q's norms in the rows' factors.  Stacking the query's rows
+// under the key's makes each product 128 rows tall, so the outputs cost no
+// product of their own, and the value of a row of [k; q] S^T or [T; M T] X is
+// in one thread's reach: X, u' and y are elementwise.  The state stays in
+// registers in fp32 (thread: one n, 32 or 16 of the tile's rows).  Operands
+// that the kernels compute (T, M T, S, X, u') are split in two bf16 parts and
+// their products taken part by part without lo x lo: 16 bits; one bf16
+// rounding of the state would leave 2^-9 in every chunk.
+//
+// The decays' exponents are differences of the prefix sums, which are taken
+// in fp64 and kept as two floats: the sums reach hundreds, the differences of
+// neighbours matter.  A token's Delta A is held above -200 (exp(-200) is 0 in
+// fp32, so nothing changes) to keep the sums finite.
+constexpr int kGdrC = 64;             // tokens per chunk
+constexpr int kGdrTile = 64;          // state rows per CTA of the scan
+constexpr int kGdrPrepThreads = 128;
+constexpr int kGdrWarps = 8;          // elementwise warps of the scan
+constexpr int kGdrScanThreads = 32 * (kGdrWarps + 2);
+
+struct GdrChunkParams {
+    const __nv_bfloat16* v;       // [B][L] rows of [H][P], v_stride elements between tokens
+    const __nv_bfloat16* dt;      // [B][L][H]
+    const __nv_bfloat16* beta;    // [B][L][H]
+    const float* dt_bias;         // [H] or null
+    const float* A;               // [H]
+    const float* h_in;            // [B][H][P][N] or null
+    __nv_bfloat16* y;             // [B][L][H][P]
+    float* h_out;                 // [B][H][P][N]
+    float4* fac;                  // [B][chunks][H][64] per token: X's, u's and y's factor, the chunk's decay
+    int64_t L, v_stride;
+    int H, G, P;
+    int chunk0, chunks;           // this launch's chunks of the sequence
+    float scale, eps;
+    unsigned wait_limit;
+    unsigned long long* status;
+    unsigned long long status_epoch;
+};
+
+__device__ __forceinline__ void gdr_fail(const GdrChunkParams& p) {
+    atomicOr(&g_mm_fault, 1u);
+    if (p.status) atomicExch(p.status, (p.status_epoch << 8) | 1ull);
+}
+
+// v[8] -> one 16-byte piece of each part
+__device__ __forceinline__ void split_store8(const float* v, unsigned char* hi_p, unsigned char* lo_p) {
+    uint4 hi, lo;
+    split_bf16x2(v[0], v[1], hi.x, lo.x);
+    split_bf16x2(v[2], v[3], hi.y, lo.y);
+    split_bf16x2(v[4], v[5], hi.z, lo.z);
+    split_bf16x2(v[6], v[7], hi.w, lo.w);
+    *reinterpret_cast<uint4*>(hi_p) = hi;
+    *reinterpret_cast<uint4*>(lo_p) = lo;
+}
+
+template <int N>
+struct GdrPrepLayout {
+    static constexpr int ld = kGdrC + 4;                          // fp32 rows, 16-byte pieces of 8 rows on different banks
+    static constexpr int kq_bytes = 2 * kGdrC * N * 2;            // [k; q]: a [128][64] block per 64 of N
+    static constexpr int t_bytes = 2 * kGdrC * 128;               // [T; M T], one part
+    static constexpr int mat_bytes = kGdrC * ld * 4;
+    // L, its inverse and a product of two blocks (fp32) lie over k and q once
+    // [k; q] k^T is taken, the rows [T; M T] over those once T is read
+    static constexpr int l_off = 0;
+    static constexpr int inv_off = mat_bytes;
+    static constexpr int work_off = 2 * mat_bytes;
+    static constexpr int big = work_off + 32 * 36 * 4;
+    static constexpr int kq_off = 0, t_off = 0;
+    static constexpr int m_off = (big + 1023) / 1024 * 1024;
+    static_assert(m_off >= kq_bytes && m_off >= 2 * t_bytes, "k and q, and the operand rows, fit below M");
+    static constexpr int f_off = m_off + 2 * kGdrC * 128;
+    static constexpr int floats = 5 * kGdrC;
+    static constexpr int bar_off = f_off + floats * 4 + 32;
+    static constexpr int smem_bytes = 1024 + bar_off + 3 * 8 + 16;
+};
+
+template <int N>
+__global__ void __launch_bounds__(kGdrPrepThreads)
+gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_t)
+{
+    using Lay = GdrPrepLayout<N>;
+    constexpr int ld = Lay::ld;
+    extern __shared__ __align__(1024) unsigned char gdp_raw[];
+    unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(gdp_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* kq = sm + Lay::kq_off;
+    float* Lm = reinterpret_cast<float*>(sm + Lay::l_off);
+    float* Tm = reinterpret_cast<float*>(sm + Lay::inv_off);
+    float* Wm = reinterpret_cast<float*>(sm + Lay::work_off);
+    unsigned char* mt = sm + Lay::m_off;                 // M hi, lo: 64 rows each
+    unsigned char* tt = sm + Lay::t_off;                 // [T; M T] hi, lo: 128 rows each
+    float* cum_hi = reinterpret_cast<float*>(sm + Lay::f_off);
+    float* cum_lo = cum_hi + kGdrC;
+    float* bt = cum_lo + kGdrC;                          // b_t
+    float* rk = bt + kGdrC;                              // 1 / |k_t| or 1
+    float* rq = rk + kGdrC;                              // scale / |q_t| or scale
+    double* half_sum = reinterpret_cast<double*>(rq + kGdrC);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Lay::bar_off);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3);
+
+    const int c = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t t0 = static_cast<int64_t>(p.chunk0 + c) * kGdrC;
+    const int64_t unit = (static_cast<int64_t>(b) * p.chunks + c) * p.H + h;
+    const int g = h / (p.H / p.G);
+    if (p.status && tid == 0 && c == 0 && h == 0 && b == 0) p.status[1] = p.status_epoch;
+
+    if (tid == 0) {
+        mbar_init(&bars[0], 1);
+        mbar_init(&bars[1], 1);
+        mbar_init(&bars[2], 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(&bars[0], Lay::kq_bytes);
+        for (int kb = 0; kb < N / 64; ++kb) {     // rows past the sequence read as zeros
+            tma_load_3d(kq + kb * 16384, &tm_k, g * N + kb * 64, static_cast<int>(t0), b, &bars[0]);
+            tma_load_3d(kq + kb * 16384 + 8192, &tm_q, g * N + kb * 64, static_cast<int>(t0), b, &bars[0]);
+        }
+    }
+    if (warp == 2) {
+        tmem_alloc(tmem_slot, 128);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    // decays and write strengths; a token past the sequence has a = 1, b = 0
+    double cum = 0.0;
+    if (tid < kGdrC) {
+        float la = 0.0f, be = 0.0f;
+        if (t0 + tid < p.L) {
+            const int64_t o = (static_cast<int64_t>(b) * p.L + t0 + tid) * p.H + h;
+            la = MathExact::step(__bfloat162float(p.dt[o]), p.dt_bias ? p.dt_bias[h] : 0.0f) * p.A[h];
+            la = la < -200.0f ? -200.0f : la;         // a NaN stays
+            be = 1.0f / (1.0f + expf(-__bfloat162float(p.beta[o])));
+        }
+        cum = static_cast<double>(la);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double n = __shfl_up_sync(kFull, cum, o);
+            if (lane >= o) cum += n;
+        }
+        if (tid == 31) *half_sum = cum;
+        bt[tid] = be;
+    }
+    __syncthreads();
+    if (tid < kGdrC) {
+        if (warp == 1) cum += *half_sum;
+        const float hi = static_cast<float>(cum);
+        cum_hi[tid] = hi;
+        cum_lo[tid] = static_cast<float>(cum - static_cast<double>(hi));
+    }
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+
+    // [k; q] k^T
+    bool ok = mbar_wait_bounded(&bars[0], 0, p.wait_limit);
+    const bool loaded = __syncthreads_and(ok);
+    if (loaded) {
+        if (warp == 1 && elect_one_lane()) {
+            constexpr uint32_t idesc = umma_idesc_bf16(2 * kGdrC, kGdrC);
+#pragma unroll
+            for (int kk = 0; kk < N / 16; ++kk) {
+                const uint64_t d = umma_desc_sw128(smem_addr(kq) + (kk >> 2) * 16384 + (kk & 3) * 32);
+                umma_bf16(tmem, d, d, idesc, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(&bars[1]);
+        }
+        // the norm of row tid: a token's k (rows 0..63) or q
+        float s = 0.0f;
+#pragma unroll
+        for (int kb = 0; kb < N / 64; ++kb)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint4 w = *reinterpret_cast<const uint4*>(kq + kb * 16384 + sw128_off(tid, q));
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s = fmaf(bf16_lo(ws[e]), bf16_lo(ws[e]), fmaf(bf16_hi(ws[e]), bf16_hi(ws[e]), s));
+            }
+        const float r = p.eps > 0.0f ? rsqrtf(s + p.eps) : 1.0f;
+        if (tid < kGdrC) rk[tid] = r;
+        else rq[tid - kGdrC] = r * p.scale;
+    }
+    __syncthreads();
+    if (tid < kGdrC) {
+        const float gam = expf(cum_hi[tid]);
+        const float last = expf((cum_hi[kGdrC - 1] - cum_hi[tid]) + (cum_lo[kGdrC - 1] - cum_lo[tid]));
+        p.fac[unit * kGdrC + tid] = make_float4(gam * rk[tid], last * rk[tid], gam * rq[tid], expf(cum_hi[kGdrC - 1]));
+    }
+    if (loaded) ok = mbar_wait_bounded(&bars[1], 0, p.wait_limit);
+    tc_fence_after();
+    const bool ready = __syncthreads_and(ok) && loaded;
+
+    // row i of L (warps 0, 1) or of M (warps 2, 3); columns past the row's
+    // 32-column block are zero
+    if (ready) {
+        const int i = tid & (kGdrC - 1);
+        const bool key = tid < kGdrC;
+        const float ch = cum_hi[i], cl = cum_lo[i];
+        const float ri = key ? bt[i] * rk[i] : rq[i];
+#pragma unroll 1
+        for (int jb = 0; jb < 2; ++jb) {
+            float m[32];
+            if (jb <= (warp & 1)) {
+                tmem_ld32(lane_base + jb * 32, m);
+#pragma unroll
+                for (int q = 0; q < 32; ++q) {
+                    const int j = jb * 32 + q;
+                    const float e = expf((ch - cum_hi[j]) + (cl - cum_lo[j]));
+                    m[q] = (key ? j < i : j <= i) ? m[q] * (ri * rk[j]) * e : 0.0f;
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 32; ++q) m[q] = 0.0f;
+            }
+            if (key) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    *reinterpret_cast<float4*>(Lm + i * ld + jb * 32 + 4 * q) = make_float4(m[4 * q], m[4 * q + 1], m[4 * q + 2], m[4 * q + 3]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t off = sw128_off(i, jb * 4 + q);
+                    split_store8(m + 8 * q, mt + off, mt + 8192 + off);
+                }
+            }
+        }
+    }
+    __syncthreads();
+
+    // T = (I + L)^-1 in fp32: the four 16 x 16 diagonal blocks by substitution,
+    // then twice [[P, 0], [R, Q]]^-1 = [[P^-1, 0], [-Q^-1 R P^-1, Q^-1]]
+    if (tid < kGdrC) {
+        const int d = tid >> 4, col = tid & 15;
+        float x[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const float* row = Lm + (16 * d + r) * ld + 16 * d;
+            float s = r == col ? 1.0f : 0.0f;
+#pragma unroll
+            for (int l = 0; l < r; ++l) s = fmaf(-row[l], x[l], s);
+            x[r] = s;
+            Tm[(16 * d + r) * ld + 16 * d + col] = s;
+        }
+    } else {
+        // zeros right of the diagonal blocks
+        const int i = tid - kGdrC;
+        for (int j = (i / 16 + 1) * 16; j < kGdrC; j += 4) *reinterpret_cast<float4*>(Tm + i * ld + j) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncthreads();
+    // W = R P^-1, then -Q^-1 W, for the blocks of S rows: pair s0, thread's rows and four columns
+    {
+        const int pair = tid >> 6, i = (tid & 63) >> 2, j = (tid & 3) * 4;      // 16 x 16 of each of two pairs
+        const int o = pair * 32;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int l = 0; l < 16; ++l) {
+            const float a = Lm[(o + 16 + i) * ld + o + l];
+            const float4 t = *reinterpret_cast<const float4*>(Tm + (o + l) * ld + o + j);
+            s.x = fmaf(a, t.x, s.x); s.y = fmaf(a, t.y, s.y); s.z = fmaf(a, t.z, s.z); s.w = fmaf(a, t.w, s.w);
+        }
+        *reinterpret_cast<float4*>(Wm + (pair * 16 + i) * 36 + j) = s;
+        __syncthreads();
+        s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int l = 0; l < 16; ++l) {
+            const float a = -Tm[(o + 16 + i) * ld + o + 16 + l];
+            const float4 t = *reinterpret_cast<const float4*>(Wm + (pair * 16 + l) * 36 + j);
+            s.x = fmaf(a, t.x, s.x); s.y = fmaf(a, t.y, s.y); s.z = fmaf(a, t.z, s.z); s.w = fmaf(a, t.w, s.w);
+        }
+        *reinterpret_cast<float4*>(Tm + (o + 16 + i) * ld + o + j) = s;
+    }
+    __syncthreads();
+    {
+        const int i = (tid >> 3) * 2, j = (tid & 7) * 4;       // 32 x 32: two rows, four columns
+        float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 8
+        for (int l = 0; l < 32; ++l) {
+            const float4 t = *reinterpret_cast<const float4*>(Tm + l * ld + j);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float a = Lm[(32 + i + r) * ld + l];
+                s[r].x = fmaf(a, t.x, s[r].x); s[r].y = fmaf(a, t.y, s[r].y); s[r].z = fmaf(a, t.z, s[r].z); s[r].w = fmaf(a, t.w, s[r].w);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) *reinterpret_cast<float4*>(Wm + (i + r) * 36 + j) = s[r];
+        __syncthreads();
+        s[0] = s[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int l = 0; l < 32; ++l) {
+            const float4 t = *reinterpret_cast<const float4*>(Wm + l * 36 + j);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float a = -Tm[(32 + i + r) * ld + 32 + l];
+                s[r].x = fmaf(a, t.x, s[r].x); s[r].y = fmaf(a, t.y, s[r].y); s[r].z = fmaf(a, t.z, s[r].z); s[r].w = fmaf(a, t.w, s[r].w);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) *reinterpret_cast<float4*>(Tm + (32 + i + r) * ld + j) = s[r];
+    }
+    __syncthreads();
+    // T diag(b), split, as rows 0..63 of the operand tile
+    {
+        const int i = tid & (kGdrC - 1), hf = tid >> 6;
+        float t[32];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const float4 v = *reinterpret_cast<const float4*>(Tm + i * ld + hf * 32 + 4 * q);
+            const float4 s = *reinterpret_cast<const float4*>(bt + hf * 32 + 4 * q);
+            t[4 * q] = v.x * s.x;
+            t[4 * q + 1] = v.y * s.y;
+            t[4 * q + 2] = v.z * s.z;
+            t[4 * q + 3] = v.w * s.w;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t off = sw128_off(i, hf * 4 + q);
+            split_store8(t + 8 * q, tt + off, tt + Lay::t_bytes + off);
+        }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // M T: A = the 128 rows that end with M's (the 64 before them are whatever
+    // precedes the tile, and their results are not read); B = T [l][j], MN-major
+    if (ready && warp == 1 && elect_one_lane()) {
+        constexpr uint32_t idesc = umma_idesc_bf16_mn(2 * kGdrC, kGdrC, false, true);
+        const uint32_t mh = smem_addr(mt) - 8192, ml = smem_addr(mt), th = smem_addr(tt), tl = th + Lay::t_bytes;
+#pragma unroll
+        for (int kk = 0; kk < kGdrC / 16; ++kk) {
+            umma_bf16(tmem + 64, umma_desc_sw128(mh + kk * 32), umma_desc_sw128_mn(th + kk * 2048, 0), idesc, kk > 0 ? 1u : 0u);
+            umma_bf16(tmem + 64, umma_desc_sw128(mh + kk * 32), umma_desc_sw128_mn(tl + kk * 2048, 0), idesc, 1u);
+            umma_bf16(tmem + 64, umma_desc_sw128(ml + kk * 32), umma_desc_sw128_mn(th + kk * 2048, 0), idesc, 1u);
+        }
+        umma_commit(&bars[2]);
+    }
+    bool done = false;
+    if (ready) done = mbar_wait_bounded(&bars[2], 0, p.wait_limit);
+    tc_fence_after();
+    if (done && warp >= 2) {
+#pragma unroll 1
+        for (int jb = 0; jb < 2; ++jb) {
+            float m[32];
+            tmem_ld32(lane_base + 64 + jb * 32, m);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t off = sw128_off(tid, jb * 4 + q);
+                split_store8(m + 8 * q, tt + off, tt + Lay::t_bytes + off);
+            }
+        }
+        fence_proxy_async_smem();
+    }
+    if (__syncthreads_and(done)) {
+        if (tid == 0) {
+            tma_store_2d(&tm_t, tt, 0, static_cast<int>(unit * 256));
+            tma_store_2d(&tm_t, tt + Lay::t_bytes, 0, static_cast<int>(unit * 256 + 128));
+            bulk_commit_group();
+            bulk_wait_read_all();
+        }
+    } else {
+        if (tid == 0) gdr_fail(p);
+        // the copies and products finish before shared and tensor memory go away
+        if (warp == 1 && elect_one_lane()) {
+            if (!loaded) mbar_wait_bounded(&bars[0], 0, 1u << 20);
+            else mbar_wait_bounded(&bars[ready ? 2 : 1], 0, 1u << 20);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 128);
+    }
+}
+
+template <int N>
+struct GdrScanLayout {
+    static constexpr int kq_bytes = 2 * kGdrC * N * 2;          // [k; q]
+    static constexpr int t_bytes = 2 * kGdrC * 128;             // one part of [T; M T]
+    static constexpr int s_bytes = N * 128;                     // one part of S^T [n][64 rows]
+    static constexpr int x_bytes = kGdrC * 128;                 // one part of X or u' [token][64 rows]
+    static constexpr int stages = 2;
+    static constexpr int t_off = stages * kq_bytes;
+    static constexpr int s_off = t_off + stages * 2 * t_bytes;
+    static constexpr int x_off = s_off + 2 * s_bytes;
+    static constexpr int bar_off = x_off + 2 * x_bytes;
+    static constexpr int bars = 4 * stages + 6;
+    static constexpr int smem_bytes = 1024 + bar_off + bars * 8 + 16;
+};
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" :: "r"(smem_addr(bar)) : "memory");
+}
+// COLS consecutive fp32 columns of this thread's row of tensor memory
+template <int COLS>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[COLS]) {
+    if constexpr (COLS == 32) {
+        tmem_ld32(taddr, v);
+    } else {
+        static_assert(COLS == 16, "16 or 32 columns");
+        uint32_t r[16];
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr));
+        asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+    }
+}
+
+// the same answer for every lane of the warp
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned limit) {
+    return __all_sync(kFull, mbar_wait_bounded(bar, parity, limit));
+}
+
+// Eight elementwise warps, one that issues the products and one that copies.
+// Warp w reaches the tensor-memory lanes of quarter w % 4 and takes columns
+// 32 (w / 4).. of its rows: quarters 0 and 1 hold the tokens' keys (X and u'),
+// 2 and 3 their queries (y).  With N = 64 product 3 takes the 64 rows of k^T
+// twice (both 64-row blocks of the operand at one address), so that all four
+// quarters hold the state, 16 columns a thread.
+template <int N>
+__global__ void __launch_bounds__(kGdrScanThreads, 1)
+gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_t)
+{
+    using Lay = GdrScanLayout<N>;
+    constexpr int kStages = Lay::stages;
+    constexpr int kCols = N == 128 ? 32 : 16;            // state entries per thread
+    constexpr uint32_t kD1 = 0, kD2 = 64, kD3 = 128, kTmemCols = 256;
+    extern __shared__ __align__(1024) unsigned char gds_raw[];
+    unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(gds_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + Lay::bar_off);
+    uint64_t* kq_free = kq_full + kStages;
+    uint64_t* t_full = kq_free + kStages;
+    uint64_t* t_free = t_full + kStages;
+    uint64_t* d_full = t_free + kStages;                 // [3] products 1, 2, 3
+    uint64_t* in_full = d_full + 3;                      // [3] S, X, u' written
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + 3);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tile = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int g = h / (p.H / p.G);
+    const int n_chunks = p.chunks;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&kq_full[s], 1);
+            mbar_init(&kq_free[s], 1);
+            mbar_init(&t_full[s], 1);
+            mbar_init(&t_free[s], 1);
+        }
+        for (int i = 0; i < 3; ++i) mbar_init(&d_full[i], 1);
+        mbar_init(&in_full[0], kGdrWarps);
+        mbar_init(&in_full[1], kGdrWarps / 2);
+        mbar_init(&in_full[2], kGdrWarps / 2);
+        fence_mbar_init();
+    }
+    if (warp == kGdrWarps) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+    int issued = 0;          // the copying lane: chunks requested; the other: products committed
+
+    if (warp == kGdrWarps + 1) {
+        if (elect_one_lane()) {
+            for (int c = 0; c < n_chunks && ok; ++c) {
+                const int s = c % kStages;
+                const unsigned par = static_cast<unsigned>(((c / kStages) & 1) ^ 1);
+                unsigned char* kq = sm + s * Lay::kq_bytes;
+                unsigned char* tt = sm + Lay::t_off + s * 2 * Lay::t_bytes;
+                const int tok = (p.chunk0 + c) * kGdrC;
+                if (!(ok = mbar_wait_bounded(&kq_free[s], par, p.wait_limit))) break;
+                mbar_arrive_expect_tx(&kq_full[s], Lay::kq_bytes);
+                for (int kb = 0; kb < N / 64; ++kb) {
+                    tma_load_3d(kq + kb * 16384, &tm_k, g * N + kb * 64, tok, b, &kq_full[s]);
+                    tma_load_3d(kq + kb * 16384 + 8192, &tm_q, g * N + kb * 64, tok, b, &kq_full[s]);
+                }
+                ++issued;
+                if (!(ok = mbar_wait_bounded(&t_free[s], par, p.wait_limit))) break;
+                const int row = static_cast<int>(((static_cast<int64_t>(b) * p.chunks + c) * p.H + h) * 256);
+                mbar_arrive_expect_tx(&t_full[s], 2 * Lay::t_bytes);
+                tma_load_2d(tt, &tm_t, 0, row, &t_full[s]);
+                tma_load_2d(tt + Lay::t_bytes, &tm_t, 0, row + 128, &t_full[s]);
+                ++issued;
+            }
+        }
+    } else if (warp == kGdrWarps) {
+        if (elect_one_lane()) {
+            constexpr uint32_t id_12 = umma_idesc_bf16_mn(2 * kGdrC, kGdrTile, false, true);
+            constexpr uint32_t id_3 = umma_idesc_bf16_mn(128, kGdrTile, true, true);
+            const uint32_t sh = smem_addr(sm + Lay::s_off), sl = sh + Lay::s_bytes;
+            const uint32_t xh = smem_addr(sm + Lay::x_off), xl = xh + Lay::x_bytes;
+            for (int c = 0; c < n_chunks; ++c) {
+                const int s = c % kStages;
+                const unsigned par = static_cast<unsigned>(c & 1), spar = static_cast<unsigned>((c / kStages) & 1);
+                const uint32_t kq = smem_addr(sm + s * Lay::kq_bytes);
+                const uint32_t th = smem_addr(sm + Lay::t_off + s * 2 * Lay::t_bytes), tl = th + Lay::t_bytes;
+                if (!(ok = mbar_wait_bounded(&kq_full[s], spar, p.wait_limit) &&
+                           mbar_wait_bounded(&in_full[0], par, p.wait_limit))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < N / 16; ++kk) {
+                    const uint64_t a = umma_desc_sw128(kq + (kk >> 2) * 16384 + (kk & 3) * 32);
+                    umma_bf16(tmem + kD1, a, umma_desc_sw128_mn(sh + kk * 2048, 0), id_12, kk > 0 ? 1u : 0u);
+                    umma_bf16(tmem + kD1, a, umma_desc_sw128_mn(sl + kk * 2048, 0), id_12, 1u);
+                }
+                umma_commit(&d_full[0]);
+                ++issued;
+                if (!(ok = mbar_wait_bounded(&t_full[s], spar, p.wait_limit) &&
+                           mbar_wait_bounded(&in_full[1], par, p.wait_limit))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < kGdrC / 16; ++kk) {
+                    const uint64_t ah = umma_desc_sw128(th + kk * 32), al = umma_desc_sw128(tl + kk * 32);
+                    const uint64_t bh = umma_desc_sw128_mn(xh + kk * 2048, 0);
+                    umma_bf16(tmem + kD2, ah, bh, id_12, kk > 0 ? 1u : 0u);
+                    umma_bf16(tmem + kD2, ah, umma_desc_sw128_mn(xl + kk * 2048, 0), id_12, 1u);
+                    umma_bf16(tmem + kD2, al, bh, id_12, 1u);
+                }
+                umma_commit(&d_full[1]);
+                umma_commit(&t_free[s]);
+                ++issued;
+                if (!(ok = mbar_wait_bounded(&in_full[2], par, p.wait_limit))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < kGdrC / 16; ++kk) {
+                    const uint64_t a = umma_desc_sw128_mn(kq + kk * 2048, N == 128 ? 16384 : 0);
+                    umma_bf16(tmem + kD3, a, umma_desc_sw128_mn(xh + kk * 2048, 0), id_3, kk > 0 ? 1u : 0u);
+                    umma_bf16(tmem + kD3, a, umma_desc_sw128_mn(xl + kk * 2048, 0), id_3, 1u);
+                }
+                umma_commit(&d_full[2]);
+                umma_commit(&kq_free[s]);
+                ++issued;
+            }
+        }
+    } else {
+        const int q = warp & 3, wg = warp >> 2;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        const int i = (q & 1) * 32 + lane;                                   // this thread's token of a chunk
+        const int col0 = wg * 32;                                            // its 32 of the tile's rows
+        const int n = N == 128 ? q * 32 + lane : (q & 1) * 32 + lane;        // its state: entry n
+        const int srow0 = N == 128 ? wg * 32 : wg * 32 + (q >> 1) * 16;      // of these rows of the tile
+        unsigned char* sp = sm + Lay::s_off;
+        unsigned char* xp = sm + Lay::x_off;
+        float S[kCols];
+        const int64_t state = ((static_cast<int64_t>(b) * p.H + h) * p.P + tile * kGdrTile + srow0) * N + n;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) S[j] = p.h_in ? p.h_in[state + static_cast<int64_t>(j) * N] : 0.0f;
+
+        uint4 vn[4];
+        float4 fn;
+        auto fetch = [&](int c) {
+            const int64_t t = static_cast<int64_t>(p.chunk0 + c) * kGdrC + i;
+            fn = p.fac[((static_cast<int64_t>(b) * p.chunks + c) * p.H + h) * kGdrC + i];
+            if (q < 2) {
+                const uint4* src = reinterpret_cast<const uint4*>(p.v + (static_cast<int64_t>(b) * p.L + t) * p.v_stride +
+                                                                  static_cast<int64_t>(h) * p.P + tile * kGdrTile + col0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) vn[k] = t < p.L ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        fetch(0);
+        for (int c = 0; c < n_chunks; ++c) {
+            const unsigned par = static_cast<unsigned>(c & 1);
+            // S's parts, entry n of the tile's rows
+#pragma unroll
+            for (int k = 0; k < kCols / 8; ++k) {
+                const uint32_t off = sw128_off(n, srow0 / 8 + k);
+                split_store8(S + 8 * k, sp + off, sp + Lay::s_bytes + off);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (elect_one_lane()) mbar_arrive(&in_full[0]);
+
+            const float4 f = fn;
+            if (!(ok = warp_wait(&d_full[0], par, p.wait_limit))) break;
+            tc_fence_after();
+            float d[32];
+            tmem_ld32(lane_base + kD1 + col0, d);
+            if (q < 2) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t w[4] = {vn[k].x, vn[k].y, vn[k].z, vn[k].w};
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[2 * e] = fmaf(-f.x, d[8 * k + 2 * e], bf16_lo(w[e]));
+                        x[2 * e + 1] = fmaf(-f.x, d[8 * k + 2 * e + 1], bf16_hi(w[e]));
+                    }
+                    const uint32_t off = sw128_off(i, wg * 4 + k);
+                    split_store8(x, xp + off, xp + Lay::x_bytes + off);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (elect_one_lane()) mbar_arrive(&in_full[1]);
+            }
+            if (c + 1 < n_chunks) fetch(c + 1);
+            if (!(ok = warp_wait(&d_full[1], par, p.wait_limit))) break;
+            tc_fence_after();
+            float u[32];
+            tmem_ld32(lane_base + kD2 + col0, u);
+            if (q < 2) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u[8 * k + e] *= f.y;
+                    const uint32_t off = sw128_off(i, wg * 4 + k);
+                    split_store8(u + 8 * k, xp + off, xp + Lay::x_bytes + off);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (elect_one_lane()) mbar_arrive(&in_full[2]);
+            } else {
+                const int64_t t = static_cast<int64_t>(p.chunk0 + c) * kGdrC + i;
+                if (t < p.L) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.y + ((static_cast<int64_t>(b) * p.L + t) * p.H + h) * p.P +
+                                                          tile * kGdrTile + col0);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_bf16x2(fmaf(f.z, d[8 * k + 2 * e], u[8 * k + 2 * e]),
+                                               fmaf(f.z, d[8 * k + 2 * e + 1], u[8 * k + 2 * e + 1]));
+                        dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            if (!(ok = warp_wait(&d_full[2], par, p.wait_limit))) break;
+            tc_fence_after();
+            float add[kCols];
+            tmem_ld_cols<kCols>(lane_base + kD3 + srow0, add);
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) S[j] = fmaf(f.w, S[j], add[j]);
+        }
+        if (ok) {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) p.h_out[state + static_cast<int64_t>(j) * N] = S[j];
+        }
+    }
+    tc_fence_before();
+    if (!__syncthreads_and(ok)) {
+        if (tid == 0) gdr_fail(p);
+        // the copies and products in flight finish before shared and tensor memory go away
+        if (warp == kGdrWarps + 1 && elect_one_lane()) {
+            for (int k = max(0, issued - 2 * kStages); k < issued; ++k) {
+                const int c = k / 2, s = c % kStages;
+                mbar_wait_bounded(k % 2 ? &t_full[s] : &kq_full[s], static_cast<unsigned>((c / kStages) & 1), 1u << 20);
+            }
+        } else if (warp == kGdrWarps && elect_one_lane() && issued > 0) {
+            const int k = issued - 1;
+            mbar_wait_bounded(&d_full[k % 3], static_cast<unsigned>((k / 3) & 1), 1u << 20);
+        }
+        __syncthreads();
+    }
+    if (warp == kGdrWarps) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
 }
 
 }  // namespace mm

@@ -1959,6 +1959,90 @@ mm_status launch_gdr_recurrent(const mm::GdrParams& p, const GdrArgs& a, cudaStr
     return e == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
+// The chunked form: bf16 calls of at least kGdrChunkedMin tokens whose copies'
+// coordinates and strides fit (a workspace row index in 31 bits, a tensor's
+// strides in 40).  The chunks run in rounds of as many as bring the workspace
+// to kGdrRoundUnits chunks of a head, each round from the state that the one
+// before left in h_last.
+constexpr int64_t kGdrChunkedMin = 24;
+constexpr int64_t kGdrRoundUnits = 16384;      // 33 KB each
+struct GdrPlan {
+    bool chunked = false;
+    int64_t chunks = 0, round = 0;             // of a sequence; of a launch
+    size_t off_fac = 0, off_t = 0, total = kWsHeader;
+};
+GdrPlan plan_gdr(int64_t batch, int64_t seqlen, int64_t heads, mm_dtype act) {
+    GdrPlan pl;
+    if (act != MM_BF16 || seqlen < kGdrChunkedMin || batch * heads > (int64_t(1) << 20)) return pl;
+    pl.chunked = true;
+    pl.chunks = (seqlen + mm::kGdrC - 1) / mm::kGdrC;
+    pl.round = std::min(pl.chunks, std::max<int64_t>(1, kGdrRoundUnits / (batch * heads)));
+    const int64_t units = batch * heads * pl.round;
+    pl.off_fac = kWsHeader;
+    pl.off_t = pl.off_fac + static_cast<size_t>(units) * mm::kGdrC * 16;
+    pl.total = pl.off_t + static_cast<size_t>(units) * 2 * (2 * mm::kGdrC * 128);
+    return pl;
+}
+
+// 3-D map over the rows of q or k: [batch][tokens][cols], tokens `stride`
+// elements apart, boxes of 64 tokens x 64 columns in the 128-byte swizzle.
+bool encode_gdr_rows(CUtensorMap* m, const void* base, int64_t cols, int64_t stride, int64_t seqlen, int64_t batch) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(seqlen), static_cast<cuuint64_t>(batch)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride * 2), static_cast<cuuint64_t>(seqlen * stride * 2)};
+    const cuuint32_t box[3] = {64, mm::kGdrC, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int N>
+mm_status launch_gdr_chunked(const GdrArgs& a, const GdrPlan& pl, unsigned char* w, unsigned long long epoch, cudaStream_t s) {
+    CUtensorMap tq, tk, tt;
+    if (!encode_gdr_rows(&tq, a.q, a.groups * N, a.q_stride, a.seqlen, a.batch) ||
+        !encode_gdr_rows(&tk, a.k, a.groups * N, a.k_stride, a.seqlen, a.batch) ||
+        !encode_gemm_2d(&tt, w + pl.off_t, 64, a.batch * a.heads * pl.round * 256, 128))
+        return MM_ERR_CUDA;
+    static std::atomic<unsigned long long> allowed_prep{0}, allowed_scan{0};
+    if (allow_smem(mm::gdr_prep_kernel<N>, allowed_prep) != cudaSuccess ||
+        allow_smem(mm::gdr_scan_kernel<N>, allowed_scan) != cudaSuccess) { cudaGetLastError(); return MM_ERR_CUDA; }
+    mm::GdrChunkParams p{};
+    p.v = static_cast<const __nv_bfloat16*>(a.v);
+    p.dt = static_cast<const __nv_bfloat16*>(a.dt);
+    p.beta = static_cast<const __nv_bfloat16*>(a.beta);
+    p.dt_bias = a.dt_bias;
+    p.A = a.A;
+    p.h_in = a.h0;
+    p.y = static_cast<__nv_bfloat16*>(a.y);
+    p.h_out = a.h_last;
+    p.fac = reinterpret_cast<float4*>(w + pl.off_fac);
+    p.L = a.seqlen;
+    p.v_stride = a.v_stride;
+    p.H = static_cast<int>(a.heads);
+    p.G = static_cast<int>(a.groups);
+    p.P = static_cast<int>(a.headdim);
+    p.scale = a.scale;
+    p.eps = a.norm_eps;
+    p.wait_limit = copy_wait_limit();
+    p.status = reinterpret_cast<unsigned long long*>(w);
+    p.status_epoch = epoch;
+    const bool fail = forced_launch_failure();
+    for (int64_t c0 = 0; c0 < pl.chunks; c0 += pl.round) {
+        p.chunk0 = static_cast<int>(c0);
+        p.chunks = static_cast<int>(std::min(pl.round, pl.chunks - c0));
+        if (c0 > 0) p.h_in = a.h_last;
+        mm::gdr_prep_kernel<N><<<dim3(static_cast<unsigned>(p.chunks), static_cast<unsigned>(p.H), static_cast<unsigned>(a.batch)),
+                                 mm::kGdrPrepThreads, fail ? (1 << 20) : mm::GdrPrepLayout<N>::smem_bytes, s>>>(p, tq, tk, tt);
+        if (cudaGetLastError() != cudaSuccess) return MM_ERR_CUDA;
+        mm::gdr_scan_kernel<N><<<dim3(static_cast<unsigned>(p.P / mm::kGdrTile), static_cast<unsigned>(p.H), static_cast<unsigned>(a.batch)),
+                                 mm::kGdrScanThreads, fail ? (1 << 20) : mm::GdrScanLayout<N>::smem_bytes, s>>>(p, tq, tk, tt);
+        if (cudaGetLastError() != cudaSuccess) return MM_ERR_CUDA;
+    }
+    return MM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1968,7 +2052,7 @@ size_t mamba_gdr_workspace_size(int64_t batch, int64_t seqlen, int64_t heads, in
     if ((act != MM_F32 && act != MM_BF16) || batch <= 0 || !gdr_sizes_ok(batch, seqlen, groups, heads) ||
         !gdr_supported(headdim, d_state))
         return 0;
-    return kWsHeader;
+    return plan_gdr(batch, seqlen, heads, act).total;
 }
 
 mm_status mamba_gdr_fwd(const void* q, const void* k, const void* v, const void* dt, const void* beta,
@@ -1982,7 +2066,8 @@ mm_status mamba_gdr_fwd(const void* q, const void* k, const void* v, const void*
     Span ins[8], outs[2];
     if (mm_status st = validate_gdr(a, false, ins, outs); st != MM_OK) return st;
     if (batch == 0) return MM_OK;
-    const size_t need = mamba_gdr_workspace_size(batch, seqlen, heads, headdim, d_state, groups, act);
+    const GdrPlan pl = plan_gdr(batch, seqlen, heads, act);
+    const size_t need = pl.total;
     if (!workspace || workspace_bytes < need) return MM_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MM_ERR_ALIGN;
     const Span sw = span(workspace, static_cast<int64_t>(need));
@@ -1990,9 +2075,15 @@ mm_status mamba_gdr_fwd(const void* q, const void* k, const void* v, const void*
         if (overlaps(sw, in)) return MM_ERR_ALIAS;
     if (overlaps(sw, outs[0]) || overlaps(sw, outs[1])) return MM_ERR_ALIAS;
     if (mm_status st = check_device(); st != MM_OK) return st;
+    const unsigned long long epoch = next_call_id();
+    if (pl.chunked) {
+        unsigned char* w = static_cast<unsigned char*>(workspace);
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        return d_state == 64 ? launch_gdr_chunked<64>(a, pl, w, epoch, s) : launch_gdr_chunked<128>(a, pl, w, epoch, s);
+    }
     mm::GdrParams p = gdr_params(a);
     p.status = static_cast<unsigned long long*>(workspace);
-    p.status_epoch = next_call_id();
+    p.status_epoch = epoch;
     return launch_gdr_recurrent(p, a, static_cast<cudaStream_t>(stream));
 }
 
