@@ -227,7 +227,6 @@ constexpr int kGdrWarps = 8;          // elementwise warps of the scan
 constexpr int kGdrScanThreads = 32 * (kGdrWarps + 2);
 
 struct GdrChunkParams {
-    const __nv_bfloat16* v;       // [B][L] rows of [H][P], v_stride elements between tokens
     const __nv_bfloat16* dt;      // [B][L][H]
     const __nv_bfloat16* beta;    // [B][L][H]
     const float* dt_bias;         // [H] or null
@@ -236,7 +235,7 @@ struct GdrChunkParams {
     __nv_bfloat16* y;             // [B][L][H][P]
     float* h_out;                 // [B][H][P][N]
     float4* fac;                  // [B][chunks][H][64] per token: X's, u's and y's factor, the chunk's decay
-    int64_t L, v_stride;
+    int64_t L;
     int H, G, P;
     int chunk0, chunks;           // this launch's chunks of the sequence
     float scale, eps;
@@ -585,11 +584,14 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
 template <int N>
 struct GdrScanLayout {
     static constexpr int kq_bytes = 2 * kGdrC * N * 2;          // [k; q]
+    static constexpr int v_off = kq_bytes;                      // then v [token][64 rows] and the tokens' factors
+    static constexpr int fac_off = v_off + kGdrC * 128;
+    static constexpr int in_bytes = fac_off + kGdrC * 16;
     static constexpr int t_bytes = 2 * kGdrC * 128;             // one part of [T; M T]
     static constexpr int s_bytes = N * 128;                     // one part of S^T [n][64 rows]
     static constexpr int x_bytes = kGdrC * 128;                 // one part of X or u' [token][64 rows]
     static constexpr int stages = 2;
-    static constexpr int t_off = stages * kq_bytes;
+    static constexpr int t_off = stages * in_bytes;
     static constexpr int s_off = t_off + stages * 2 * t_bytes;
     static constexpr int x_off = s_off + 2 * s_bytes;
     static constexpr int bar_off = x_off + 2 * x_bytes;
@@ -600,26 +602,46 @@ struct GdrScanLayout {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" :: "r"(smem_addr(bar)) : "memory");
 }
-// COLS consecutive fp32 columns of this thread's row of tensor memory
-template <int COLS>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[COLS]) {
-    if constexpr (COLS == 32) {
-        tmem_ld32(taddr, v);
-    } else {
-        static_assert(COLS == 16, "16 or 32 columns");
-        uint32_t r[16];
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
-            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-            : "r"(taddr));
-        asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+// One contiguous bulk copy global -> shared (16-byte aligned, a multiple of 16
+// bytes), completion on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* gsrc, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n"
+                 :: "r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(bytes), "r"(smem_addr(bar)) : "memory");
+}
+// true in one lane of a converged warp, in a form that keeps the other
+// operands of what it guards in uniform registers (a tcgen05.mma takes those:
+// 32 to 64 cycles apart then, 46 and more when each operand is moved there
+// from one lane's registers first)
+__device__ __forceinline__ bool elect_sync() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+// 16 consecutive fp32 columns of this thread's row of tensor memory, without
+// waiting: the registers are valid after tmem_wait_ld
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// v[0..15] = the sums of 16 columns at `taddr` and the 16 that are 64 further
+// on: a product's two parts
+__device__ __forceinline__ void tmem_ld_sum16(uint32_t taddr, float* v) {
+    uint32_t hi[16], lo[16];
+    tmem_ld16_async(taddr, hi);
+    tmem_ld16_async(taddr + 64, lo);
+    tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 16; i += 2) {
+        const float2 r = __fadd2_rn(f2(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
+                                    f2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
+        v[i] = r.x;
+        v[i + 1] = r.y;
     }
 }
-
 // the same answer for every lane of the warp
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned limit) {
     return __all_sync(kFull, mbar_wait_bounded(bar, parity, limit));
@@ -634,12 +656,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsign
 template <int N>
 __global__ void __launch_bounds__(kGdrScanThreads, 1)
 gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                const __grid_constant__ CUtensorMap tm_t)
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_t)
 {
     using Lay = GdrScanLayout<N>;
     constexpr int kStages = Lay::stages;
     constexpr int kCols = N == 128 ? 32 : 16;            // state entries per thread
-    constexpr uint32_t kD1 = 0, kD2 = 64, kD3 = 128, kTmemCols = 256;
+    constexpr uint32_t kD1 = 0, kD2 = 128, kD3 = 256, kTmemCols = 512;    // a product: 64 columns of either part
     extern __shared__ __align__(1024) unsigned char gds_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(gds_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + Lay::bar_off);
@@ -684,18 +706,21 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
             for (int c = 0; c < n_chunks && ok; ++c) {
                 const int s = c % kStages;
                 const unsigned par = static_cast<unsigned>(((c / kStages) & 1) ^ 1);
-                unsigned char* kq = sm + s * Lay::kq_bytes;
+                unsigned char* kq = sm + s * Lay::in_bytes;
                 unsigned char* tt = sm + Lay::t_off + s * 2 * Lay::t_bytes;
                 const int tok = (p.chunk0 + c) * kGdrC;
                 if (!(ok = mbar_wait_bounded(&kq_free[s], par, p.wait_limit))) break;
-                mbar_arrive_expect_tx(&kq_full[s], Lay::kq_bytes);
+                const int64_t unit = (static_cast<int64_t>(b) * p.chunks + c) * p.H + h;
+                mbar_arrive_expect_tx(&kq_full[s], Lay::in_bytes);
                 for (int kb = 0; kb < N / 64; ++kb) {
                     tma_load_3d(kq + kb * 16384, &tm_k, g * N + kb * 64, tok, b, &kq_full[s]);
                     tma_load_3d(kq + kb * 16384 + 8192, &tm_q, g * N + kb * 64, tok, b, &kq_full[s]);
                 }
+                tma_load_3d(kq + Lay::v_off, &tm_v, h * p.P + tile * kGdrTile, tok, b, &kq_full[s]);
+                bulk_load(kq + Lay::fac_off, p.fac + unit * kGdrC, kGdrC * 16, &kq_full[s]);
                 ++issued;
                 if (!(ok = mbar_wait_bounded(&t_free[s], par, p.wait_limit))) break;
-                const int row = static_cast<int>(((static_cast<int64_t>(b) * p.chunks + c) * p.H + h) * 256);
+                const int row = static_cast<int>(unit * 256);
                 mbar_arrive_expect_tx(&t_full[s], 2 * Lay::t_bytes);
                 tma_load_2d(tt, &tm_t, 0, row, &t_full[s]);
                 tma_load_2d(tt + Lay::t_bytes, &tm_t, 0, row + 128, &t_full[s]);
@@ -703,53 +728,52 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
             }
         }
     } else if (warp == kGdrWarps) {
-        if (elect_one_lane()) {
-            constexpr uint32_t id_12 = umma_idesc_bf16_mn(2 * kGdrC, kGdrTile, false, true);
-            constexpr uint32_t id_3 = umma_idesc_bf16_mn(128, kGdrTile, true, true);
-            const uint32_t sh = smem_addr(sm + Lay::s_off), sl = sh + Lay::s_bytes;
-            const uint32_t xh = smem_addr(sm + Lay::x_off), xl = xh + Lay::x_bytes;
-            for (int c = 0; c < n_chunks; ++c) {
-                const int s = c % kStages;
-                const unsigned par = static_cast<unsigned>(c & 1), spar = static_cast<unsigned>((c / kStages) & 1);
-                const uint32_t kq = smem_addr(sm + s * Lay::kq_bytes);
-                const uint32_t th = smem_addr(sm + Lay::t_off + s * 2 * Lay::t_bytes), tl = th + Lay::t_bytes;
-                if (!(ok = mbar_wait_bounded(&kq_full[s], spar, p.wait_limit) &&
-                           mbar_wait_bounded(&in_full[0], par, p.wait_limit))) break;
-                tc_fence_after();
+        // Each product's second operand has its two parts side by side, 128
+        // columns wide: 64 cycles a K step of 16 for both, where two products
+        // of 64 columns take 49 each (bound by the first operand's reads).
+        constexpr uint32_t id_12 = umma_idesc_bf16_mn(2 * kGdrC, 2 * kGdrTile, false, true);
+        constexpr uint32_t id_lo = umma_idesc_bf16_mn(2 * kGdrC, kGdrTile, false, true);
+        constexpr uint32_t id_3 = umma_idesc_bf16_mn(128, 2 * kGdrTile, true, true);
+        const uint32_t sh = smem_addr(sm + Lay::s_off), xh = smem_addr(sm + Lay::x_off);
+        for (int c = 0; c < n_chunks; ++c) {
+            const int s = c % kStages;
+            const unsigned par = static_cast<unsigned>(c & 1), spar = static_cast<unsigned>((c / kStages) & 1);
+            const uint32_t kq = smem_addr(sm + s * Lay::in_bytes);
+            const uint32_t th = smem_addr(sm + Lay::t_off + s * 2 * Lay::t_bytes), tl = th + Lay::t_bytes;
+            if (!(ok = warp_wait(&kq_full[s], spar, p.wait_limit) && warp_wait(&in_full[0], par, p.wait_limit))) break;
+            tc_fence_after();
+            if (elect_sync()) {
 #pragma unroll
-                for (int kk = 0; kk < N / 16; ++kk) {
-                    const uint64_t a = umma_desc_sw128(kq + (kk >> 2) * 16384 + (kk & 3) * 32);
-                    umma_bf16(tmem + kD1, a, umma_desc_sw128_mn(sh + kk * 2048, 0), id_12, kk > 0 ? 1u : 0u);
-                    umma_bf16(tmem + kD1, a, umma_desc_sw128_mn(sl + kk * 2048, 0), id_12, 1u);
-                }
+                for (int kk = 0; kk < N / 16; ++kk)
+                    umma_bf16(tmem + kD1, umma_desc_sw128(kq + (kk >> 2) * 16384 + (kk & 3) * 32),
+                              umma_desc_sw128_mn(sh + kk * 2048, Lay::s_bytes), id_12, kk > 0 ? 1u : 0u);
                 umma_commit(&d_full[0]);
-                ++issued;
-                if (!(ok = mbar_wait_bounded(&t_full[s], spar, p.wait_limit) &&
-                           mbar_wait_bounded(&in_full[1], par, p.wait_limit))) break;
-                tc_fence_after();
+            }
+            ++issued;
+            if (!(ok = warp_wait(&t_full[s], spar, p.wait_limit) && warp_wait(&in_full[1], par, p.wait_limit))) break;
+            tc_fence_after();
+            if (elect_sync()) {
 #pragma unroll
                 for (int kk = 0; kk < kGdrC / 16; ++kk) {
-                    const uint64_t ah = umma_desc_sw128(th + kk * 32), al = umma_desc_sw128(tl + kk * 32);
-                    const uint64_t bh = umma_desc_sw128_mn(xh + kk * 2048, 0);
-                    umma_bf16(tmem + kD2, ah, bh, id_12, kk > 0 ? 1u : 0u);
-                    umma_bf16(tmem + kD2, ah, umma_desc_sw128_mn(xl + kk * 2048, 0), id_12, 1u);
-                    umma_bf16(tmem + kD2, al, bh, id_12, 1u);
+                    umma_bf16(tmem + kD2, umma_desc_sw128(th + kk * 32), umma_desc_sw128_mn(xh + kk * 2048, Lay::x_bytes),
+                              id_12, kk > 0 ? 1u : 0u);
+                    umma_bf16(tmem + kD2, umma_desc_sw128(tl + kk * 32), umma_desc_sw128_mn(xh + kk * 2048, 0), id_lo, 1u);
                 }
                 umma_commit(&d_full[1]);
                 umma_commit(&t_free[s]);
-                ++issued;
-                if (!(ok = mbar_wait_bounded(&in_full[2], par, p.wait_limit))) break;
-                tc_fence_after();
+            }
+            ++issued;
+            if (!(ok = warp_wait(&in_full[2], par, p.wait_limit))) break;
+            tc_fence_after();
+            if (elect_sync()) {
 #pragma unroll
-                for (int kk = 0; kk < kGdrC / 16; ++kk) {
-                    const uint64_t a = umma_desc_sw128_mn(kq + kk * 2048, N == 128 ? 16384 : 0);
-                    umma_bf16(tmem + kD3, a, umma_desc_sw128_mn(xh + kk * 2048, 0), id_3, kk > 0 ? 1u : 0u);
-                    umma_bf16(tmem + kD3, a, umma_desc_sw128_mn(xl + kk * 2048, 0), id_3, 1u);
-                }
+                for (int kk = 0; kk < kGdrC / 16; ++kk)
+                    umma_bf16(tmem + kD3, umma_desc_sw128_mn(kq + kk * 2048, N == 128 ? 16384 : 0),
+                              umma_desc_sw128_mn(xh + kk * 2048, Lay::x_bytes), id_3, kk > 0 ? 1u : 0u);
                 umma_commit(&d_full[2]);
                 umma_commit(&kq_free[s]);
-                ++issued;
             }
+            ++issued;
         }
     } else {
         const int q = warp & 3, wg = warp >> 2;
@@ -765,48 +789,55 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
 #pragma unroll
         for (int j = 0; j < kCols; ++j) S[j] = p.h_in ? p.h_in[state + static_cast<int64_t>(j) * N] : 0.0f;
 
-        uint4 vn[4];
-        float4 fn;
-        auto fetch = [&](int c) {
+        // y of a chunk, stored once the next chunk's first operand is written:
+        // the fence before that waits for the memory operations before it
+        uint32_t yw[16];
+        auto store_y = [&](int c) {
             const int64_t t = static_cast<int64_t>(p.chunk0 + c) * kGdrC + i;
-            fn = p.fac[((static_cast<int64_t>(b) * p.chunks + c) * p.H + h) * kGdrC + i];
-            if (q < 2) {
-                const uint4* src = reinterpret_cast<const uint4*>(p.v + (static_cast<int64_t>(b) * p.L + t) * p.v_stride +
-                                                                  static_cast<int64_t>(h) * p.P + tile * kGdrTile + col0);
+            if (t < p.L) {
+                uint4* dst = reinterpret_cast<uint4*>(p.y + ((static_cast<int64_t>(b) * p.L + t) * p.H + h) * p.P +
+                                                      tile * kGdrTile + col0);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) vn[k] = t < p.L ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+                for (int k = 0; k < 4; ++k) dst[k] = make_uint4(yw[4 * k], yw[4 * k + 1], yw[4 * k + 2], yw[4 * k + 3]);
             }
         };
-        fetch(0);
         for (int c = 0; c < n_chunks; ++c) {
+            const int s = c % kStages;
             const unsigned par = static_cast<unsigned>(c & 1);
+            const unsigned char* in = sm + s * Lay::in_bytes;
             // S's parts, entry n of the tile's rows
 #pragma unroll
             for (int k = 0; k < kCols / 8; ++k) {
                 const uint32_t off = sw128_off(n, srow0 / 8 + k);
                 split_store8(S + 8 * k, sp + off, sp + Lay::s_bytes + off);
             }
+            if (!(ok = warp_wait(&kq_full[s], static_cast<unsigned>((c / kStages) & 1), p.wait_limit))) break;
+            const float4 f = *reinterpret_cast<const float4*>(in + Lay::fac_off + i * 16);
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (elect_one_lane()) mbar_arrive(&in_full[0]);
+            if (q >= 2 && c > 0) store_y(c - 1);
 
-            const float4 f = fn;
             if (!(ok = warp_wait(&d_full[0], par, p.wait_limit))) break;
             tc_fence_after();
             float d[32];
-            tmem_ld32(lane_base + kD1 + col0, d);
+            tmem_ld_sum16(lane_base + kD1 + col0, d);
+            tmem_ld_sum16(lane_base + kD1 + col0 + 16, d + 16);
             if (q < 2) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t w[4] = {vn[k].x, vn[k].y, vn[k].z, vn[k].w};
+                    const uint32_t off = sw128_off(i, wg * 4 + k);
+                    const uint4 v = *reinterpret_cast<const uint4*>(in + Lay::v_off + off);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        x[2 * e] = fmaf(-f.x, d[8 * k + 2 * e], bf16_lo(w[e]));
-                        x[2 * e + 1] = fmaf(-f.x, d[8 * k + 2 * e + 1], bf16_hi(w[e]));
+                        const float2 r = fma2(f2(-f.x, -f.x), f2(d[8 * k + 2 * e], d[8 * k + 2 * e + 1]),
+                                              f2(bf16_lo(w[e]), bf16_hi(w[e])));
+                        x[2 * e] = r.x;
+                        x[2 * e + 1] = r.y;
                     }
-                    const uint32_t off = sw128_off(i, wg * 4 + k);
                     split_store8(x, xp + off, xp + Lay::x_bytes + off);
                 }
                 fence_proxy_async_smem();
@@ -814,11 +845,11 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 __syncwarp();
                 if (elect_one_lane()) mbar_arrive(&in_full[1]);
             }
-            if (c + 1 < n_chunks) fetch(c + 1);
             if (!(ok = warp_wait(&d_full[1], par, p.wait_limit))) break;
             tc_fence_after();
             float u[32];
-            tmem_ld32(lane_base + kD2 + col0, u);
+            tmem_ld_sum16(lane_base + kD2 + col0, u);
+            tmem_ld_sum16(lane_base + kD2 + col0 + 16, u + 16);
             if (q < 2) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -832,28 +863,19 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 __syncwarp();
                 if (elect_one_lane()) mbar_arrive(&in_full[2]);
             } else {
-                const int64_t t = static_cast<int64_t>(p.chunk0 + c) * kGdrC + i;
-                if (t < p.L) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.y + ((static_cast<int64_t>(b) * p.L + t) * p.H + h) * p.P +
-                                                          tile * kGdrTile + col0);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack_bf16x2(fmaf(f.z, d[8 * k + 2 * e], u[8 * k + 2 * e]),
-                                               fmaf(f.z, d[8 * k + 2 * e + 1], u[8 * k + 2 * e + 1]));
-                        dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
+                for (int e = 0; e < 16; ++e)
+                    yw[e] = pack_bf16x2(fmaf(f.z, d[2 * e], u[2 * e]), fmaf(f.z, d[2 * e + 1], u[2 * e + 1]));
             }
             if (!(ok = warp_wait(&d_full[2], par, p.wait_limit))) break;
             tc_fence_after();
             float add[kCols];
-            tmem_ld_cols<kCols>(lane_base + kD3 + srow0, add);
+#pragma unroll
+            for (int k = 0; k < kCols; k += 16) tmem_ld_sum16(lane_base + kD3 + srow0 + k, add + k);
 #pragma unroll
             for (int j = 0; j < kCols; ++j) S[j] = fmaf(f.w, S[j], add[j]);
         }
+        if (ok && q >= 2) store_y(n_chunks - 1);
         if (ok) {
 #pragma unroll
             for (int j = 0; j < kCols; ++j) p.h_out[state + static_cast<int64_t>(j) * N] = S[j];

@@ -1984,7 +1984,7 @@ GdrPlan plan_gdr(int64_t batch, int64_t seqlen, int64_t heads, mm_dtype act) {
     return pl;
 }
 
-// 3-D map over the rows of q or k: [batch][tokens][cols], tokens `stride`
+// 3-D map over the rows of q, k or v: [batch][tokens][cols], tokens `stride`
 // elements apart, boxes of 64 tokens x 64 columns in the 128-byte swizzle.
 bool encode_gdr_rows(CUtensorMap* m, const void* base, int64_t cols, int64_t stride, int64_t seqlen, int64_t batch) {
     auto enc = tensor_map_encoder();
@@ -2000,16 +2000,16 @@ bool encode_gdr_rows(CUtensorMap* m, const void* base, int64_t cols, int64_t str
 
 template <int N>
 mm_status launch_gdr_chunked(const GdrArgs& a, const GdrPlan& pl, unsigned char* w, unsigned long long epoch, cudaStream_t s) {
-    CUtensorMap tq, tk, tt;
+    CUtensorMap tq, tk, tv, tt;
     if (!encode_gdr_rows(&tq, a.q, a.groups * N, a.q_stride, a.seqlen, a.batch) ||
         !encode_gdr_rows(&tk, a.k, a.groups * N, a.k_stride, a.seqlen, a.batch) ||
+        !encode_gdr_rows(&tv, a.v, a.heads * a.headdim, a.v_stride, a.seqlen, a.batch) ||
         !encode_gemm_2d(&tt, w + pl.off_t, 64, a.batch * a.heads * pl.round * 256, 128))
         return MM_ERR_CUDA;
     static std::atomic<unsigned long long> allowed_prep{0}, allowed_scan{0};
     if (allow_smem(mm::gdr_prep_kernel<N>, allowed_prep) != cudaSuccess ||
         allow_smem(mm::gdr_scan_kernel<N>, allowed_scan) != cudaSuccess) { cudaGetLastError(); return MM_ERR_CUDA; }
     mm::GdrChunkParams p{};
-    p.v = static_cast<const __nv_bfloat16*>(a.v);
     p.dt = static_cast<const __nv_bfloat16*>(a.dt);
     p.beta = static_cast<const __nv_bfloat16*>(a.beta);
     p.dt_bias = a.dt_bias;
@@ -2019,7 +2019,6 @@ mm_status launch_gdr_chunked(const GdrArgs& a, const GdrPlan& pl, unsigned char*
     p.h_out = a.h_last;
     p.fac = reinterpret_cast<float4*>(w + pl.off_fac);
     p.L = a.seqlen;
-    p.v_stride = a.v_stride;
     p.H = static_cast<int>(a.heads);
     p.G = static_cast<int>(a.groups);
     p.P = static_cast<int>(a.headdim);
@@ -2037,7 +2036,7 @@ mm_status launch_gdr_chunked(const GdrArgs& a, const GdrPlan& pl, unsigned char*
                                  mm::kGdrPrepThreads, fail ? (1 << 20) : mm::GdrPrepLayout<N>::smem_bytes, s>>>(p, tq, tk, tt);
         if (cudaGetLastError() != cudaSuccess) return MM_ERR_CUDA;
         mm::gdr_scan_kernel<N><<<dim3(static_cast<unsigned>(p.P / mm::kGdrTile), static_cast<unsigned>(p.H), static_cast<unsigned>(a.batch)),
-                                 mm::kGdrScanThreads, fail ? (1 << 20) : mm::GdrScanLayout<N>::smem_bytes, s>>>(p, tq, tk, tt);
+                                 mm::kGdrScanThreads, fail ? (1 << 20) : mm::GdrScanLayout<N>::smem_bytes, s>>>(p, tq, tk, tv, tt);
         if (cudaGetLastError() != cudaSuccess) return MM_ERR_CUDA;
     }
     return MM_OK;
