@@ -223,7 +223,7 @@ gdr_recurrent_kernel(const GdrParams p)
 constexpr int kGdrC = 64;             // tokens per chunk
 constexpr int kGdrTile = 64;          // state rows per CTA of the scan
 constexpr int kGdrPrepThreads = 128;
-constexpr int kGdrWarps = 8;          // elementwise warps of the scan
+constexpr int kGdrWarps = 16;         // elementwise warps of the scan
 constexpr int kGdrScanThreads = 32 * (kGdrWarps + 2);
 
 struct GdrChunkParams {
@@ -627,32 +627,38 @@ __device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
-// v[0..15] = the sums of 16 columns at `taddr` and the 16 that are 64 further
-// on: a product's two parts
-__device__ __forceinline__ void tmem_ld_sum16(uint32_t taddr, float* v) {
-    uint32_t hi[16], lo[16];
-    tmem_ld16_async(taddr, hi);
-    tmem_ld16_async(taddr + 64, lo);
+__device__ __forceinline__ void tmem_ld8_async(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+// v = the sums of COLS columns at `taddr` and as many 64 further on: a
+// product's two parts
+template <int COLS>
+__device__ __forceinline__ void tmem_ld_sum(uint32_t taddr, float (&v)[COLS]) {
+    uint32_t hi[COLS], lo[COLS];
+    if constexpr (COLS == 16) {
+        tmem_ld16_async(taddr, hi);
+        tmem_ld16_async(taddr + 64, lo);
+    } else {
+        tmem_ld8_async(taddr, hi);
+        tmem_ld8_async(taddr + 64, lo);
+    }
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        const float2 r = __fadd2_rn(f2(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
-                                    f2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
-        v[i] = r.x;
-        v[i + 1] = r.y;
-    }
+    for (int i = 0; i < COLS; ++i) v[i] = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
 }
 // the same answer for every lane of the warp
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned limit) {
     return __all_sync(kFull, mbar_wait_bounded(bar, parity, limit));
 }
 
-// Eight elementwise warps, one that issues the products and one that copies.
+// 16 elementwise warps, one that issues the products and one that copies.
 // Warp w reaches the tensor-memory lanes of quarter w % 4 and takes columns
-// 32 (w / 4).. of its rows: quarters 0 and 1 hold the tokens' keys (X and u'),
+// 16 (w / 4).. of its rows: quarters 0 and 1 hold the tokens' keys (X and u'),
 // 2 and 3 their queries (y).  With N = 64 product 3 takes the 64 rows of k^T
 // twice (both 64-row blocks of the operand at one address), so that all four
-// quarters hold the state, 16 columns a thread.
+// quarters hold the state, 8 columns a thread instead of 16.
 template <int N>
 __global__ void __launch_bounds__(kGdrScanThreads, 1)
 gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -660,7 +666,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
 {
     using Lay = GdrScanLayout<N>;
     constexpr int kStages = Lay::stages;
-    constexpr int kCols = N == 128 ? 32 : 16;            // state entries per thread
+    constexpr int kCols = N == 128 ? 16 : 8;             // state entries per thread
     constexpr uint32_t kD1 = 0, kD2 = 128, kD3 = 256, kTmemCols = 512;    // a product: 64 columns of either part
     extern __shared__ __align__(1024) unsigned char gds_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(gds_raw) + 1023) & ~uintptr_t(1023));
@@ -687,7 +693,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         for (int i = 0; i < 3; ++i) mbar_init(&d_full[i], 1);
         mbar_init(&in_full[0], kGdrWarps);
         mbar_init(&in_full[1], kGdrWarps / 2);
-        mbar_init(&in_full[2], kGdrWarps / 2);
+        mbar_init(&in_full[2], kGdrWarps);
         fence_mbar_init();
     }
     if (warp == kGdrWarps) {
@@ -779,9 +785,9 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         const int q = warp & 3, wg = warp >> 2;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
         const int i = (q & 1) * 32 + lane;                                   // this thread's token of a chunk
-        const int col0 = wg * 32;                                            // its 32 of the tile's rows
+        const int col0 = wg * 16;                                            // its 16 of the tile's rows
         const int n = N == 128 ? q * 32 + lane : (q & 1) * 32 + lane;        // its state: entry n
-        const int srow0 = N == 128 ? wg * 32 : wg * 32 + (q >> 1) * 16;      // of these rows of the tile
+        const int srow0 = N == 128 ? wg * 16 : wg * 16 + (q >> 1) * 8;       // of these rows of the tile
         unsigned char* sp = sm + Lay::s_off;
         unsigned char* xp = sm + Lay::x_off;
         float S[kCols];
@@ -791,14 +797,14 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
 
         // y of a chunk, stored once the next chunk's first operand is written:
         // the fence before that waits for the memory operations before it
-        uint32_t yw[16];
+        uint32_t yw[8];
         auto store_y = [&](int c) {
             const int64_t t = static_cast<int64_t>(p.chunk0 + c) * kGdrC + i;
             if (t < p.L) {
                 uint4* dst = reinterpret_cast<uint4*>(p.y + ((static_cast<int64_t>(b) * p.L + t) * p.H + h) * p.P +
                                                       tile * kGdrTile + col0);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) dst[k] = make_uint4(yw[4 * k], yw[4 * k + 1], yw[4 * k + 2], yw[4 * k + 3]);
+                dst[0] = make_uint4(yw[0], yw[1], yw[2], yw[3]);
+                dst[1] = make_uint4(yw[4], yw[5], yw[6], yw[7]);
             }
         };
         for (int c = 0; c < n_chunks; ++c) {
@@ -811,32 +817,38 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 const uint32_t off = sw128_off(n, srow0 / 8 + k);
                 split_store8(S + 8 * k, sp + off, sp + Lay::s_bytes + off);
             }
-            if (!(ok = warp_wait(&kq_full[s], static_cast<unsigned>((c / kStages) & 1), p.wait_limit))) break;
-            const float4 f = *reinterpret_cast<const float4*>(in + Lay::fac_off + i * 16);
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (elect_one_lane()) mbar_arrive(&in_full[0]);
             if (q >= 2 && c > 0) store_y(c - 1);
 
-            if (!(ok = warp_wait(&d_full[0], par, p.wait_limit))) break;
-            tc_fence_after();
-            float d[32];
-            tmem_ld_sum16(lane_base + kD1 + col0, d);
-            tmem_ld_sum16(lane_base + kD1 + col0 + 16, d + 16);
+            if (!(ok = warp_wait(&kq_full[s], static_cast<unsigned>((c / kStages) & 1), p.wait_limit))) break;
+            const float4 f = *reinterpret_cast<const float4*>(in + Lay::fac_off + i * 16);
+            uint4 v[2];
             if (q < 2) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t off = sw128_off(i, wg * 4 + k);
-                    const uint4 v = *reinterpret_cast<const uint4*>(in + Lay::v_off + off);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                for (int k = 0; k < 2; ++k) v[k] = *reinterpret_cast<const uint4*>(in + Lay::v_off + sw128_off(i, wg * 2 + k));
+            } else {
+                // no u' of this warp's: it only must have read its factors
+                // before product 3 lets the next chunk but one overwrite them
+                __syncwarp();
+                if (elect_one_lane()) mbar_arrive(&in_full[2]);
+            }
+            if (!(ok = warp_wait(&d_full[0], par, p.wait_limit))) break;
+            tc_fence_after();
+            float d[16];
+            tmem_ld_sum<16>(lane_base + kD1 + col0, d);
+            if (q < 2) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t off = sw128_off(i, wg * 2 + k);
+                    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 r = fma2(f2(-f.x, -f.x), f2(d[8 * k + 2 * e], d[8 * k + 2 * e + 1]),
-                                              f2(bf16_lo(w[e]), bf16_hi(w[e])));
-                        x[2 * e] = r.x;
-                        x[2 * e + 1] = r.y;
+                        x[2 * e] = fmaf(-f.x, d[8 * k + 2 * e], bf16_lo(w[e]));
+                        x[2 * e + 1] = fmaf(-f.x, d[8 * k + 2 * e + 1], bf16_hi(w[e]));
                     }
                     split_store8(x, xp + off, xp + Lay::x_bytes + off);
                 }
@@ -847,15 +859,14 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
             }
             if (!(ok = warp_wait(&d_full[1], par, p.wait_limit))) break;
             tc_fence_after();
-            float u[32];
-            tmem_ld_sum16(lane_base + kD2 + col0, u);
-            tmem_ld_sum16(lane_base + kD2 + col0 + 16, u + 16);
+            float u[16];
+            tmem_ld_sum<16>(lane_base + kD2 + col0, u);
             if (q < 2) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 2; ++k) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) u[8 * k + e] *= f.y;
-                    const uint32_t off = sw128_off(i, wg * 4 + k);
+                    const uint32_t off = sw128_off(i, wg * 2 + k);
                     split_store8(u + 8 * k, xp + off, xp + Lay::x_bytes + off);
                 }
                 fence_proxy_async_smem();
@@ -864,14 +875,13 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 if (elect_one_lane()) mbar_arrive(&in_full[2]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
+                for (int e = 0; e < 8; ++e)
                     yw[e] = pack_bf16x2(fmaf(f.z, d[2 * e], u[2 * e]), fmaf(f.z, d[2 * e + 1], u[2 * e + 1]));
             }
             if (!(ok = warp_wait(&d_full[2], par, p.wait_limit))) break;
             tc_fence_after();
             float add[kCols];
-#pragma unroll
-            for (int k = 0; k < kCols; k += 16) tmem_ld_sum16(lane_base + kD3 + srow0 + k, add + k);
+            tmem_ld_sum<kCols>(lane_base + kD3 + srow0, add);
 #pragma unroll
             for (int j = 0; j < kCols; ++j) S[j] = fmaf(f.w, S[j], add[j]);
         }
