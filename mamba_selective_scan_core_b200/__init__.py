@@ -806,6 +806,59 @@ def _check_rows(t, name, dtype, shape, device):
     return heads * width if stride is None else stride
 
 
+# The calls below are made once per layer and decoded token, where a launch
+# takes a few microseconds: they look at each tensor with the fewest calls into
+# torch, and go through the checks that name what is wrong only once something is.
+def _fits(t, name, dtype, shape, dev, idx):
+    """_check, for a tensor that is given; idx is dev's index."""
+    if t.get_device() != idx or idx < 0 or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _check(t, name, dtype, shape, dev)
+
+
+def _row_stride(t, name, dtype, shape, dev, idx):
+    """_check_rows, whose common cases need no loop."""
+    if t.get_device() == idx >= 0 and t.dtype is dtype and t.shape == shape:
+        st = t.stride()
+        if st[-1] == 1 and st[-2] == shape[-1]:
+            if len(shape) == 3:
+                return st[0] if shape[0] > 1 else shape[1] * shape[2]
+            if shape[0] > 0 and shape[1] > 1 and st[0] == shape[1] * st[1]:
+                return st[1]
+    return _check_rows(t, name, dtype, shape, dev)
+
+
+class _Torch:
+    """What the calls below need of torch and of the library, looked up once."""
+
+    def __init__(self):
+        import torch
+
+        self.f32, self.bf16, self.u8 = torch.float32, torch.bfloat16, torch.uint8
+        self.codes = {torch.float32: MM_F32, torch.bfloat16: MM_BF16}
+        self.empty, self.device, self.current_device = torch.empty, torch.cuda.device, torch.cuda.current_device
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda i: torch.cuda.current_stream(i).cuda_stream)
+        self.lib = lib()
+
+
+_torch_names = None
+
+
+def _names():
+    global _torch_names
+    if _torch_names is None:
+        _torch_names = _Torch()
+    return _torch_names
+
+
+def _call_on(T, dev, idx, fn, *args):
+    """fn(*args) with dev, whose index is idx, as the current device."""
+    if T.current_device() == idx:
+        return fn(*args)
+    with T.device(dev):
+        return fn(*args)
+
+
 def gdr_workspace_size(batch, seqlen, heads, headdim=128, d_state=128, groups=1, act=MM_BF16) -> int:
     return int(lib().mamba_gdr_workspace_size(batch, seqlen, heads, headdim, d_state, groups, act))
 
@@ -819,42 +872,50 @@ def gdr_fwd(q, k, v, dt, beta, dt_bias, A, h0=None, *, scale=None, norm_eps=1e-6
     to N ** -0.5; q and k are L2-normalised with norm_eps, or used as they are
     when it is 0.  Returns (y [B,L,H,P], h_last [B,H,P,N] fp32), allocating any
     output not given."""
-    import torch
-
-    f32 = torch.float32
-    act = _act_code(v.dtype)
+    T = _torch_names or _names()
+    f32, dtype = T.f32, v.dtype
+    act = T.codes.get(dtype)
+    if act is None:
+        _act_code(dtype)
     Bsz, L, H, P = v.shape
-    G, N = q.shape[2], q.shape[3]
-    dev = v.device
+    G, N = q.shape[2:]
+    dev, idx = v.device, v.get_device()
     made = []
-    qs = _check_rows(q, "q", v.dtype, (Bsz, L, G, N), dev)
-    ks = _check_rows(k, "k", v.dtype, (Bsz, L, G, N), dev)
-    vs = _check_rows(v, "v", v.dtype, (Bsz, L, H, P), dev)
-    _check(dt, "dt", v.dtype, (Bsz, L, H), dev)
-    _check(beta, "beta", v.dtype, (Bsz, L, H), dev)
-    _check(dt_bias, "dt_bias", f32, (H,), dev)
-    _check(A, "A", f32, (H,), dev)
-    _check(h0, "h0", f32, (Bsz, H, P, N), dev)
+    qs = _row_stride(q, "q", dtype, (Bsz, L, G, N), dev, idx)
+    ks = _row_stride(k, "k", dtype, (Bsz, L, G, N), dev, idx)
+    vs = _row_stride(v, "v", dtype, (Bsz, L, H, P), dev, idx)
+    _fits(dt, "dt", dtype, (Bsz, L, H), dev, idx)
+    _fits(beta, "beta", dtype, (Bsz, L, H), dev, idx)
+    _fits(A, "A", f32, (H,), dev, idx)
+    if dt_bias is not None:
+        _fits(dt_bias, "dt_bias", f32, (H,), dev, idx)
+    state = (Bsz, H, P, N)
+    if h0 is not None:
+        _fits(h0, "h0", f32, state, dev, idx)
     if y is None:
-        y = torch.empty((Bsz, L, H, P), dtype=v.dtype, device=dev)
+        y = T.empty((Bsz, L, H, P), dtype=dtype, device=dev)
         made.append(y)
+    else:
+        _fits(y, "y", dtype, (Bsz, L, H, P), dev, idx)
     if h_last is None:
-        h_last = torch.empty((Bsz, H, P, N), dtype=f32, device=dev)
+        h_last = T.empty(state, dtype=f32, device=dev)
         made.append(h_last)
-    _check(y, "y", v.dtype, (Bsz, L, H, P), dev)
-    _check(h_last, "h_last", f32, (Bsz, H, P, N), dev)
-    with torch.cuda.device(dev):
-        ws_bytes = gdr_workspace_size(Bsz, L, H, P, N, G, act)
-        if workspace is None or workspace.numel() * workspace.element_size() < ws_bytes:
-            workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=dev)
-            made.append(workspace)
-        st = lib().mamba_gdr_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(dt_bias), _ptr(A), _ptr(h0),
-                                 _ptr(y), _ptr(h_last), Bsz, L, G, H, P, N, qs, ks, vs,
-                                 float(N ** -0.5 if scale is None else scale), float(norm_eps), act, _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    else:
+        _fits(h_last, "h_last", f32, state, dev, idx)
+    ws_bytes = T.lib.mamba_gdr_workspace_size(Bsz, L, H, P, N, G, act)
+    have = 0 if workspace is None else workspace.nbytes
+    if workspace is None or have < ws_bytes:
+        have = max(ws_bytes, 256)
+        workspace = T.empty(have, dtype=T.u8, device=dev)
+        made.append(workspace)
+    st = _call_on(T, dev, idx, T.lib.mamba_gdr_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), beta.data_ptr(),
+                  None if dt_bias is None else dt_bias.data_ptr(), A.data_ptr(), None if h0 is None else h0.data_ptr(),
+                  y.data_ptr(), h_last.data_ptr(), Bsz, L, G, H, P, N, qs, ks, vs, N ** -0.5 if scale is None else scale,
+                  norm_eps, act, workspace.data_ptr(), have, T.raw_stream(idx) if stream is None else stream.cuda_stream)
     if st != 0:
         raise MixerError(st, "mamba_gdr_fwd")
-    _keep_alive_on(made, (stream,))
+    if stream is not None:
+        _keep_alive_on(made, (stream,))
     return y, h_last
 
 
@@ -863,36 +924,38 @@ def gdr_state_update(q, k, v, dt, beta, dt_bias, A, state, *, scale=None, norm_e
     state [B,H,P,N] fp32: q, k [B,G,N] and v [B,H,P] (bf16 or fp32; rows evenly
     spaced), dt and beta [B,H], dt_bias/A [H] fp32 (dt_bias may be None).  scale
     and norm_eps as gdr_fwd.  Returns y [B,H,P], allocated if not given."""
-    import torch
-
-    f32 = torch.float32
-    act = _act_code(v.dtype)
+    T = _torch_names or _names()
+    f32, dtype = T.f32, v.dtype
+    act = T.codes.get(dtype)
+    if act is None:
+        _act_code(dtype)
     Bsz, H, P = v.shape
-    G, N = q.shape[1], q.shape[2]
-    dev = v.device
-    made = []
-    qs = _check_rows(q, "q", v.dtype, (Bsz, G, N), dev)
-    ks = _check_rows(k, "k", v.dtype, (Bsz, G, N), dev)
-    vs = _check_rows(v, "v", v.dtype, (Bsz, H, P), dev)
-    _check(dt, "dt", v.dtype, (Bsz, H), dev)
-    _check(beta, "beta", v.dtype, (Bsz, H), dev)
-    _check(dt_bias, "dt_bias", f32, (H,), dev)
-    _check(A, "A", f32, (H,), dev)
-    _check(state, "state", f32, (Bsz, H, P, N), dev)
+    G, N = q.shape[1:]
+    dev, idx = v.device, v.get_device()
+    qs = _row_stride(q, "q", dtype, (Bsz, G, N), dev, idx)
+    ks = _row_stride(k, "k", dtype, (Bsz, G, N), dev, idx)
+    vs = _row_stride(v, "v", dtype, (Bsz, H, P), dev, idx)
+    _fits(dt, "dt", dtype, (Bsz, H), dev, idx)
+    _fits(beta, "beta", dtype, (Bsz, H), dev, idx)
+    _fits(A, "A", f32, (H,), dev, idx)
+    if dt_bias is not None:
+        _fits(dt_bias, "dt_bias", f32, (H,), dev, idx)
     if state is None:
         raise ValueError("state must be given")
-    if y is None:
-        y = torch.empty((Bsz, H, P), dtype=v.dtype, device=dev)
-        made.append(y)
-    _check(y, "y", v.dtype, (Bsz, H, P), dev)
-    with torch.cuda.device(dev):
-        st = lib().mamba_gdr_state_update(_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(dt_bias), _ptr(A),
-                                          _ptr(state), _ptr(y), Bsz, G, H, P, N, qs, ks, vs,
-                                          float(N ** -0.5 if scale is None else scale), float(norm_eps), act,
-                                          _stream_handle(stream))
+    _fits(state, "state", f32, (Bsz, H, P, N), dev, idx)
+    own = y is None
+    if own:
+        y = T.empty((Bsz, H, P), dtype=dtype, device=dev)
+    else:
+        _fits(y, "y", dtype, (Bsz, H, P), dev, idx)
+    st = _call_on(T, dev, idx, T.lib.mamba_gdr_state_update, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(),
+                  beta.data_ptr(), None if dt_bias is None else dt_bias.data_ptr(), A.data_ptr(), state.data_ptr(),
+                  y.data_ptr(), Bsz, G, H, P, N, qs, ks, vs, N ** -0.5 if scale is None else scale, norm_eps, act,
+                  T.raw_stream(idx) if stream is None else stream.cuda_stream)
     if st != 0:
         raise MixerError(st, "mamba_gdr_state_update")
-    _keep_alive_on(made, (stream,))
+    if own and stream is not None:
+        y.record_stream(stream)
     return y
 
 
@@ -901,29 +964,31 @@ def proj_q4(x, W, scales, zeros=None, *, group=128, out=None, out_dtype=None, st
     (mamba_proj_q4): W [N,K/2] uint8 (even inputs in the low four bits), scales
     and zeros [N,K/group] bf16 (zeros None: 8), weight = scale (number - zero).
     out [M,N] fp32 (default) or bf16, allocated if not given."""
-    import torch
-
-    bf = torch.bfloat16
+    T = _torch_names or _names()
+    bf = T.bf16
     M, K = x.shape
     N = W.shape[0]
-    dev = x.device
+    dev, idx = x.device, x.get_device()
     if group <= 0:
         raise ValueError(f"group must be positive, got {group}")
-    _check(x, "x", bf, (M, K), dev)
-    _check(W, "W", torch.uint8, (N, K // 2), dev)
-    _check(scales, "scales", bf, (N, K // group), dev)
-    _check(zeros, "zeros", bf, (N, K // group), dev)
-    made = []
-    dtype = out_dtype or (out.dtype if out is not None else torch.float32)
-    code = _act_code(dtype)
-    if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=dev)
-        made.append(out)
-    _check(out, "out", dtype, (M, N), dev)
-    with torch.cuda.device(dev):
-        st = lib().mamba_proj_q4(_ptr(x), _ptr(W), _ptr(scales), _ptr(zeros), _ptr(out), M, N, K, group, code,
-                                 _stream_handle(stream))
+    _fits(x, "x", bf, (M, K), dev, idx)
+    _fits(W, "W", T.u8, (N, K // 2), dev, idx)
+    _fits(scales, "scales", bf, (N, K // group), dev, idx)
+    if zeros is not None:
+        _fits(zeros, "zeros", bf, (N, K // group), dev, idx)
+    dtype = out_dtype or (out.dtype if out is not None else T.f32)
+    code = T.codes.get(dtype)
+    if code is None:
+        _act_code(dtype)
+    own = out is None
+    if own:
+        out = T.empty((M, N), dtype=dtype, device=dev)
+    else:
+        _fits(out, "out", dtype, (M, N), dev, idx)
+    st = _call_on(T, dev, idx, T.lib.mamba_proj_q4, x.data_ptr(), W.data_ptr(), scales.data_ptr(),
+                  None if zeros is None else zeros.data_ptr(), out.data_ptr(), M, N, K, group, code, T.raw_stream(idx) if stream is None else stream.cuda_stream)
     if st != 0:
         raise MixerError(st, "mamba_proj_q4")
-    _keep_alive_on(made, (stream,))
+    if own and stream is not None:
+        out.record_stream(stream)
     return out

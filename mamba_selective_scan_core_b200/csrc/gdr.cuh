@@ -222,7 +222,7 @@ gdr_recurrent_kernel(const GdrParams p)
 // fp32, so nothing changes) to keep the sums finite.
 constexpr int kGdrC = 64;             // tokens per chunk
 constexpr int kGdrTile = 64;          // state rows per CTA of the scan
-constexpr int kGdrPrepThreads = 128;
+constexpr int kGdrPrepThreads = 256;
 constexpr int kGdrWarps = 16;         // elementwise warps of the scan
 constexpr int kGdrScanThreads = 32 * (kGdrWarps + 2);
 
@@ -260,6 +260,20 @@ __device__ __forceinline__ void split_store8(const float* v, unsigned char* hi_p
     *reinterpret_cast<uint4*>(lo_p) = lo;
 }
 
+// true in one lane of a converged warp, in a form that keeps the other
+// operands of what it guards in uniform registers (a tcgen05.mma takes those:
+// 32 to 64 cycles apart then, 46 and more when each operand is moved there
+// from one lane's registers first)
+__device__ __forceinline__ bool elect_sync() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+// the same answer for every lane of the warp
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned limit) {
+    return __all_sync(kFull, mbar_wait_bounded(bar, parity, limit));
+}
+
 template <int N>
 struct GdrPrepLayout {
     static constexpr int ld = kGdrC + 4;                          // fp32 rows, 16-byte pieces of 8 rows on different banks
@@ -270,8 +284,8 @@ struct GdrPrepLayout {
     // [k; q] k^T is taken, the rows [T; M T] over those once T is read
     static constexpr int l_off = 0;
     static constexpr int inv_off = mat_bytes;
-    static constexpr int work_off = 2 * mat_bytes;
-    static constexpr int big = work_off + 32 * 36 * 4;
+    static constexpr int work_off = 2 * mat_bytes;                // per n-tile of 8 columns, 32 x 8
+    static constexpr int big = work_off + 4 * 32 * 12 * 4;
     static constexpr int kq_off = 0, t_off = 0;
     static constexpr int m_off = (big + 1023) / 1024 * 1024;
     static_assert(m_off >= kq_bytes && m_off >= 2 * t_bytes, "k and q, and the operand rows, fit below M");
@@ -281,8 +295,72 @@ struct GdrPrepLayout {
     static constexpr int smem_bytes = 1024 + bar_off + 3 * 8 + 16;
 };
 
+// d += a b in fp32 on mma.m16n8k8 with tf32 operands in two parts (tf32 keeps
+// 11 bits; the second part's own cut leaves 2^-22)
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};\n"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void split_tf32(float v, uint32_t& hi, uint32_t& lo) {
+    asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(hi) : "f"(v));
+    lo = __float_as_uint(v - __uint_as_float(hi));
+}
+// D [16 MT][8] = A [16 MT][8 KT] B [8 KT][8], fp32 row-major in shared memory
+// (lda, ldb floats apart), one warp; lane 4 g + c holds rows g, g + 8 and
+// columns 2 c, 2 c + 1 of each 16 x 8 tile
+template <int MT, int KT>
+__device__ __forceinline__ void warp_matmul(float (&d)[MT][4], const float* A, int lda, const float* B, int ldb, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) d[m][0] = d[m][1] = d[m][2] = d[m][3] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+        uint32_t bh[2], bl[2];
+        split_tf32(B[(8 * k + c) * ldb + g], bh[0], bl[0]);
+        split_tf32(B[(8 * k + c + 4) * ldb + g], bh[1], bl[1]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const float* a = A + (16 * m + g) * lda + 8 * k + c;
+            uint32_t ah[4], al[4];
+            split_tf32(a[0], ah[0], al[0]);
+            split_tf32(a[8 * lda], ah[1], al[1]);
+            split_tf32(a[4], ah[2], al[2]);
+            split_tf32(a[8 * lda + 4], ah[3], al[3]);
+            mma_tf32(d[m], ah, bh);
+            mma_tf32(d[m], ah, bl);
+            mma_tf32(d[m], al, bh);
+        }
+    }
+}
+// 8 columns of the lower left block of a block triangle's inverse: W = R P^-1
+// (kept in `work`, ld 12), then -Q^-1 W, R, P^-1 and Q^-1 each 16 MT square
+template <int MT>
+__device__ __forceinline__ void inverse_columns(const float* R, const float* Pinv, const float* Qinv, int ld, float* work,
+                                                float* out, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    float d[MT][4];
+    warp_matmul<MT, 2 * MT>(d, R, ld, Pinv, ld, lane);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        *reinterpret_cast<float2*>(work + (16 * m + g) * 12 + 2 * c) = f2(d[m][0], d[m][1]);
+        *reinterpret_cast<float2*>(work + (16 * m + g + 8) * 12 + 2 * c) = f2(d[m][2], d[m][3]);
+    }
+    __syncwarp();
+    warp_matmul<MT, 2 * MT>(d, Qinv, ld, work, 12, lane);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        *reinterpret_cast<float2*>(out + (16 * m + g) * ld + 2 * c) = f2(-d[m][0], -d[m][1]);
+        *reinterpret_cast<float2*>(out + (16 * m + g + 8) * ld + 2 * c) = f2(-d[m][2], -d[m][3]);
+    }
+}
+
+// Eight warps.  Warp w reaches the tensor-memory lanes of quarter w % 4: rows
+// 32 (w % 4).. of [k; q] [k; q]^T, whose diagonal holds the norms and whose
+// columns of k, 32 (w / 4).. for this warp, become L (quarters 0 and 1) and M.
 template <int N>
-__global__ void __launch_bounds__(kGdrPrepThreads)
+__global__ void __launch_bounds__(kGdrPrepThreads, 3)
 gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_t)
 {
@@ -296,7 +374,7 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     float* Wm = reinterpret_cast<float*>(sm + Lay::work_off);
     unsigned char* mt = sm + Lay::m_off;                 // M hi, lo: 64 rows each
     unsigned char* tt = sm + Lay::t_off;                 // [T; M T] hi, lo: 128 rows each
-    float* cum_hi = reinterpret_cast<float*>(sm + Lay::f_off);
+    float* cum_hi = reinterpret_cast<float*>(sm + Lay::f_off);   // prefix sums times log2(e), hi + lo
     float* cum_lo = cum_hi + kGdrC;
     float* bt = cum_lo + kGdrC;                          // b_t
     float* rk = bt + kGdrC;                              // 1 / |k_t| or 1
@@ -307,6 +385,7 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
 
     const int c = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int q = warp & 3, half = warp >> 2;
     const int64_t t0 = static_cast<int64_t>(p.chunk0 + c) * kGdrC;
     const int64_t unit = (static_cast<int64_t>(b) * p.chunks + c) * p.H + h;
     const int g = h / (p.H / p.G);
@@ -338,7 +417,7 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
             la = la < -200.0f ? -200.0f : la;         // a NaN stays
             be = 1.0f / (1.0f + expf(-__bfloat162float(p.beta[o])));
         }
-        cum = static_cast<double>(la);
+        cum = static_cast<double>(la) * 1.4426950408889634;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const double n = __shfl_up_sync(kFull, cum, o);
@@ -356,14 +435,14 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     }
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
 
-    // [k; q] k^T
-    bool ok = mbar_wait_bounded(&bars[0], 0, p.wait_limit);
-    const bool loaded = __syncthreads_and(ok);
-    if (loaded) {
-        if (warp == 1 && elect_one_lane()) {
-            constexpr uint32_t idesc = umma_idesc_bf16(2 * kGdrC, kGdrC);
+    // [k; q] [k; q]^T
+    bool loaded = true;
+    if (warp == 7) {
+        loaded = warp_wait(&bars[0], 0, p.wait_limit);
+        if (loaded && elect_sync()) {
+            constexpr uint32_t idesc = umma_idesc_bf16(2 * kGdrC, 2 * kGdrC);
 #pragma unroll
             for (int kk = 0; kk < N / 16; ++kk) {
                 const uint64_t d = umma_desc_sw128(smem_addr(kq) + (kk >> 2) * 16384 + (kk & 3) * 32);
@@ -371,158 +450,126 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
             }
             umma_commit(&bars[1]);
         }
-        // the norm of row tid: a token's k (rows 0..63) or q
-        float s = 0.0f;
+    }
+    loaded = __syncthreads_and(loaded);
+    bool ok = loaded && warp_wait(&bars[1], 0, p.wait_limit);
+    tc_fence_after();
+    if (ok && half == 0) {
+        float m[32], s = 0.0f;
+        tmem_ld32(lane_base + q * 32, m);
 #pragma unroll
-        for (int kb = 0; kb < N / 64; ++kb)
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const uint4 w = *reinterpret_cast<const uint4*>(kq + kb * 16384 + sw128_off(tid, q));
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s = fmaf(bf16_lo(ws[e]), bf16_lo(ws[e]), fmaf(bf16_hi(ws[e]), bf16_hi(ws[e]), s));
-            }
+        for (int e = 0; e < 32; ++e) s = lane == e ? m[e] : s;
         const float r = p.eps > 0.0f ? rsqrtf(s + p.eps) : 1.0f;
-        if (tid < kGdrC) rk[tid] = r;
+        if (q < 2) rk[tid] = r;
         else rq[tid - kGdrC] = r * p.scale;
     }
-    __syncthreads();
-    if (tid < kGdrC) {
-        const float gam = expf(cum_hi[tid]);
-        const float last = expf((cum_hi[kGdrC - 1] - cum_hi[tid]) + (cum_lo[kGdrC - 1] - cum_lo[tid]));
-        p.fac[unit * kGdrC + tid] = make_float4(gam * rk[tid], last * rk[tid], gam * rq[tid], expf(cum_hi[kGdrC - 1]));
-    }
-    if (loaded) ok = mbar_wait_bounded(&bars[1], 0, p.wait_limit);
-    tc_fence_after();
-    const bool ready = __syncthreads_and(ok) && loaded;
+    const bool ready = __syncthreads_and(ok);
 
-    // row i of L (warps 0, 1) or of M (warps 2, 3); columns past the row's
-    // 32-column block are zero
+    // row i of L (quarters 0, 1) or of M, 32 columns; the columns past the
+    // row's own 32-column block are zero
     if (ready) {
-        const int i = tid & (kGdrC - 1);
-        const bool key = tid < kGdrC;
-        const float ch = cum_hi[i], cl = cum_lo[i];
-        const float ri = key ? bt[i] * rk[i] : rq[i];
-#pragma unroll 1
-        for (int jb = 0; jb < 2; ++jb) {
-            float m[32];
-            if (jb <= (warp & 1)) {
-                tmem_ld32(lane_base + jb * 32, m);
+        const int i = (q & 1) * 32 + lane;
+        const bool key = q < 2;
+        float m[32];
+        if (half <= (q & 1)) {
+            tmem_ld32(lane_base + half * 32, m);
+            const float ch = cum_hi[i], cl = cum_lo[i];
+            const float ri = key ? bt[i] * rk[i] : rq[i];
+            const int last = key ? i - 1 : i;             // the row's last column
 #pragma unroll
-                for (int q = 0; q < 32; ++q) {
-                    const int j = jb * 32 + q;
-                    const float e = expf((ch - cum_hi[j]) + (cl - cum_lo[j]));
-                    m[q] = (key ? j < i : j <= i) ? m[q] * (ri * rk[j]) * e : 0.0f;
-                }
-            } else {
-#pragma unroll
-                for (int q = 0; q < 32; ++q) m[q] = 0.0f;
+            for (int e4 = 0; e4 < 8; ++e4) {
+                const int j = half * 32 + 4 * e4;
+                const float4 jh = *reinterpret_cast<const float4*>(cum_hi + j), jl = *reinterpret_cast<const float4*>(cum_lo + j),
+                             jr = *reinterpret_cast<const float4*>(rk + j);
+                m[4 * e4] = j <= last ? m[4 * e4] * (ri * jr.x) * ex2_fast((ch - jh.x) + (cl - jl.x)) : 0.0f;
+                m[4 * e4 + 1] = j + 1 <= last ? m[4 * e4 + 1] * (ri * jr.y) * ex2_fast((ch - jh.y) + (cl - jl.y)) : 0.0f;
+                m[4 * e4 + 2] = j + 2 <= last ? m[4 * e4 + 2] * (ri * jr.z) * ex2_fast((ch - jh.z) + (cl - jl.z)) : 0.0f;
+                m[4 * e4 + 3] = j + 3 <= last ? m[4 * e4 + 3] * (ri * jr.w) * ex2_fast((ch - jh.w) + (cl - jl.w)) : 0.0f;
             }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) m[e] = 0.0f;
             if (key) {
+                // this warp has no columns of L: the tokens' factors instead
+                // (row i < 32; its lanes take tokens i and i + 32)
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    *reinterpret_cast<float4*>(Lm + i * ld + jb * 32 + 4 * q) = make_float4(m[4 * q], m[4 * q + 1], m[4 * q + 2], m[4 * q + 3]);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t off = sw128_off(i, jb * 4 + q);
-                    split_store8(m + 8 * q, mt + off, mt + 8192 + off);
+                for (int k = 0; k < 2; ++k) {
+                    const int t = lane + 32 * k;
+                    const float gam = ex2_fast(cum_hi[t] + cum_lo[t]);
+                    const float end = ex2_fast((cum_hi[kGdrC - 1] - cum_hi[t]) + (cum_lo[kGdrC - 1] - cum_lo[t]));
+                    p.fac[unit * kGdrC + t] = make_float4(gam * rk[t], end * rk[t], gam * rq[t],
+                                                          ex2_fast(cum_hi[kGdrC - 1] + cum_lo[kGdrC - 1]));
                 }
+            }
+        }
+        if (key) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<float4*>(Lm + i * ld + half * 32 + 4 * e) = make_float4(m[4 * e], m[4 * e + 1], m[4 * e + 2], m[4 * e + 3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t off = sw128_off(i, half * 4 + e);
+                split_store8(m + 8 * e, mt + off, mt + 8192 + off);
             }
         }
     }
     __syncthreads();
 
     // T = (I + L)^-1 in fp32: the four 16 x 16 diagonal blocks by substitution,
-    // then twice [[P, 0], [R, Q]]^-1 = [[P^-1, 0], [-Q^-1 R P^-1, Q^-1]]
+    // then twice [[P, 0], [R, Q]]^-1 = [[P^-1, 0], [-Q^-1 R P^-1, Q^-1]], eight
+    // columns a warp
     if (tid < kGdrC) {
         const int d = tid >> 4, col = tid & 15;
         float x[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             const float* row = Lm + (16 * d + r) * ld + 16 * d;
-            float s = r == col ? 1.0f : 0.0f;
+            float s[4] = {r == col ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int l = 0; l < r; ++l) s = fmaf(-row[l], x[l], s);
-            x[r] = s;
-            Tm[(16 * d + r) * ld + 16 * d + col] = s;
+            for (int l = 0; l < r; l += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(row + l);
+                s[0] = fmaf(-v.x, x[l], s[0]);
+                if (l + 1 < r) s[1] = fmaf(-v.y, x[l + 1], s[1]);
+                if (l + 2 < r) s[2] = fmaf(-v.z, x[l + 2], s[2]);
+                if (l + 3 < r) s[3] = fmaf(-v.w, x[l + 3], s[3]);
+            }
+            x[r] = (s[0] + s[1]) + (s[2] + s[3]);
+            Tm[(16 * d + r) * ld + 16 * d + col] = x[r];
         }
-    } else {
+    } else if (tid < 2 * kGdrC) {
         // zeros right of the diagonal blocks
         const int i = tid - kGdrC;
         for (int j = (i / 16 + 1) * 16; j < kGdrC; j += 4) *reinterpret_cast<float4*>(Tm + i * ld + j) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     __syncthreads();
-    // W = R P^-1, then -Q^-1 W, for the blocks of S rows: pair s0, thread's rows and four columns
-    {
-        const int pair = tid >> 6, i = (tid & 63) >> 2, j = (tid & 3) * 4;      // 16 x 16 of each of two pairs
-        const int o = pair * 32;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int l = 0; l < 16; ++l) {
-            const float a = Lm[(o + 16 + i) * ld + o + l];
-            const float4 t = *reinterpret_cast<const float4*>(Tm + (o + l) * ld + o + j);
-            s.x = fmaf(a, t.x, s.x); s.y = fmaf(a, t.y, s.y); s.z = fmaf(a, t.z, s.z); s.w = fmaf(a, t.w, s.w);
-        }
-        *reinterpret_cast<float4*>(Wm + (pair * 16 + i) * 36 + j) = s;
-        __syncthreads();
-        s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int l = 0; l < 16; ++l) {
-            const float a = -Tm[(o + 16 + i) * ld + o + 16 + l];
-            const float4 t = *reinterpret_cast<const float4*>(Wm + (pair * 16 + l) * 36 + j);
-            s.x = fmaf(a, t.x, s.x); s.y = fmaf(a, t.y, s.y); s.z = fmaf(a, t.z, s.z); s.w = fmaf(a, t.w, s.w);
-        }
-        *reinterpret_cast<float4*>(Tm + (o + 16 + i) * ld + o + j) = s;
+    if (warp < 4) {
+        const int o = (warp >> 1) * 32, n = (warp & 1) * 8;
+        inverse_columns<1>(Lm + (o + 16) * ld + o, Tm + o * ld + o + n, Tm + (o + 16) * ld + o + 16, ld, Wm + warp * 32 * 12,
+                           Tm + (o + 16) * ld + o + n, lane);
     }
     __syncthreads();
-    {
-        const int i = (tid >> 3) * 2, j = (tid & 7) * 4;       // 32 x 32: two rows, four columns
-        float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 8
-        for (int l = 0; l < 32; ++l) {
-            const float4 t = *reinterpret_cast<const float4*>(Tm + l * ld + j);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float a = Lm[(32 + i + r) * ld + l];
-                s[r].x = fmaf(a, t.x, s[r].x); s[r].y = fmaf(a, t.y, s[r].y); s[r].z = fmaf(a, t.z, s[r].z); s[r].w = fmaf(a, t.w, s[r].w);
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) *reinterpret_cast<float4*>(Wm + (i + r) * 36 + j) = s[r];
-        __syncthreads();
-        s[0] = s[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int l = 0; l < 32; ++l) {
-            const float4 t = *reinterpret_cast<const float4*>(Wm + l * 36 + j);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float a = -Tm[(32 + i + r) * ld + 32 + l];
-                s[r].x = fmaf(a, t.x, s[r].x); s[r].y = fmaf(a, t.y, s[r].y); s[r].z = fmaf(a, t.z, s[r].z); s[r].w = fmaf(a, t.w, s[r].w);
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) *reinterpret_cast<float4*>(Tm + (32 + i + r) * ld + j) = s[r];
-    }
+    if (warp < 4)
+        inverse_columns<2>(Lm + 32 * ld, Tm + warp * 8, Tm + 32 * ld + 32, ld, Wm + warp * 32 * 12, Tm + 32 * ld + warp * 8, lane);
     __syncthreads();
     // T diag(b), split, as rows 0..63 of the operand tile
     {
-        const int i = tid & (kGdrC - 1), hf = tid >> 6;
-        float t[32];
+        const int i = tid & (kGdrC - 1), part = tid >> 6;     // a quarter of row i
+        float t[16];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const float4 v = *reinterpret_cast<const float4*>(Tm + i * ld + hf * 32 + 4 * q);
-            const float4 s = *reinterpret_cast<const float4*>(bt + hf * 32 + 4 * q);
-            t[4 * q] = v.x * s.x;
-            t[4 * q + 1] = v.y * s.y;
-            t[4 * q + 2] = v.z * s.z;
-            t[4 * q + 3] = v.w * s.w;
+        for (int e = 0; e < 4; ++e) {
+            const float4 v = *reinterpret_cast<const float4*>(Tm + i * ld + part * 16 + 4 * e);
+            const float4 s = *reinterpret_cast<const float4*>(bt + part * 16 + 4 * e);
+            t[4 * e] = v.x * s.x;
+            t[4 * e + 1] = v.y * s.y;
+            t[4 * e + 2] = v.z * s.z;
+            t[4 * e + 3] = v.w * s.w;
         }
         __syncthreads();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t off = sw128_off(i, hf * 4 + q);
-            split_store8(t + 8 * q, tt + off, tt + Lay::t_bytes + off);
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t off = sw128_off(i, part * 2 + e);
+            split_store8(t + 8 * e, tt + off, tt + Lay::t_bytes + off);
         }
     }
     fence_proxy_async_smem();
@@ -531,30 +578,26 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     tc_fence_after();
     // M T: A = the 128 rows that end with M's (the 64 before them are whatever
     // precedes the tile, and their results are not read); B = T [l][j], MN-major
-    if (ready && warp == 1 && elect_one_lane()) {
+    if (ready && warp == 7 && elect_sync()) {
         constexpr uint32_t idesc = umma_idesc_bf16_mn(2 * kGdrC, kGdrC, false, true);
         const uint32_t mh = smem_addr(mt) - 8192, ml = smem_addr(mt), th = smem_addr(tt), tl = th + Lay::t_bytes;
 #pragma unroll
         for (int kk = 0; kk < kGdrC / 16; ++kk) {
-            umma_bf16(tmem + 64, umma_desc_sw128(mh + kk * 32), umma_desc_sw128_mn(th + kk * 2048, 0), idesc, kk > 0 ? 1u : 0u);
-            umma_bf16(tmem + 64, umma_desc_sw128(mh + kk * 32), umma_desc_sw128_mn(tl + kk * 2048, 0), idesc, 1u);
-            umma_bf16(tmem + 64, umma_desc_sw128(ml + kk * 32), umma_desc_sw128_mn(th + kk * 2048, 0), idesc, 1u);
+            umma_bf16(tmem, umma_desc_sw128(mh + kk * 32), umma_desc_sw128_mn(th + kk * 2048, 0), idesc, kk > 0 ? 1u : 0u);
+            umma_bf16(tmem, umma_desc_sw128(mh + kk * 32), umma_desc_sw128_mn(tl + kk * 2048, 0), idesc, 1u);
+            umma_bf16(tmem, umma_desc_sw128(ml + kk * 32), umma_desc_sw128_mn(th + kk * 2048, 0), idesc, 1u);
         }
         umma_commit(&bars[2]);
     }
-    bool done = false;
-    if (ready) done = mbar_wait_bounded(&bars[2], 0, p.wait_limit);
+    const bool done = ready && warp_wait(&bars[2], 0, p.wait_limit);
     tc_fence_after();
-    if (done && warp >= 2) {
-#pragma unroll 1
-        for (int jb = 0; jb < 2; ++jb) {
-            float m[32];
-            tmem_ld32(lane_base + 64 + jb * 32, m);
+    if (done && q >= 2) {
+        float m[32];
+        tmem_ld32(lane_base + half * 32, m);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t off = sw128_off(tid, jb * 4 + q);
-                split_store8(m + 8 * q, tt + off, tt + Lay::t_bytes + off);
-            }
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t off = sw128_off(q * 32 + lane, half * 4 + e);
+            split_store8(m + 8 * e, tt + off, tt + Lay::t_bytes + off);
         }
         fence_proxy_async_smem();
     }
@@ -568,7 +611,7 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     } else {
         if (tid == 0) gdr_fail(p);
         // the copies and products finish before shared and tensor memory go away
-        if (warp == 1 && elect_one_lane()) {
+        if (warp == 7 && elect_one_lane()) {
             if (!loaded) mbar_wait_bounded(&bars[0], 0, 1u << 20);
             else mbar_wait_bounded(&bars[ready ? 2 : 1], 0, 1u << 20);
         }
@@ -608,15 +651,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* gsrc, uint32_t 
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n"
                  :: "r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(bytes), "r"(smem_addr(bar)) : "memory");
 }
-// true in one lane of a converged warp, in a form that keeps the other
-// operands of what it guards in uniform registers (a tcgen05.mma takes those:
-// 32 to 64 cycles apart then, 46 and more when each operand is moved there
-// from one lane's registers first)
-__device__ __forceinline__ bool elect_sync() {
-    uint32_t p;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-    return p != 0;
-}
 // 16 consecutive fp32 columns of this thread's row of tensor memory, without
 // waiting: the registers are valid after tmem_wait_ld
 __device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
@@ -648,11 +682,6 @@ __device__ __forceinline__ void tmem_ld_sum(uint32_t taddr, float (&v)[COLS]) {
 #pragma unroll
     for (int i = 0; i < COLS; ++i) v[i] = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
 }
-// the same answer for every lane of the warp
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned limit) {
-    return __all_sync(kFull, mbar_wait_bounded(bar, parity, limit));
-}
-
 // 16 elementwise warps, one that issues the products and one that copies.
 // Warp w reaches the tensor-memory lanes of quarter w % 4 and takes columns
 // 16 (w / 4).. of its rows: quarters 0 and 1 hold the tokens' keys (X and u'),
