@@ -280,12 +280,11 @@ struct GdrPrepLayout {
     static constexpr int kq_bytes = 2 * kGdrC * N * 2;            // [k; q]: a [128][64] block per 64 of N
     static constexpr int t_bytes = 2 * kGdrC * 128;               // [T; M T], one part
     static constexpr int mat_bytes = kGdrC * ld * 4;
-    // L, its inverse and a product of two blocks (fp32) lie over k and q once
-    // [k; q] k^T is taken, the rows [T; M T] over those once T is read
+    // L and its inverse (fp32) lie over k and q once [k; q] k^T is taken, the
+    // rows [T; M T] over those once T is read
     static constexpr int l_off = 0;
     static constexpr int inv_off = mat_bytes;
-    static constexpr int work_off = 2 * mat_bytes;                // per n-tile of 8 columns, 32 x 8
-    static constexpr int big = work_off + 4 * 32 * 12 * 4;
+    static constexpr int big = 2 * mat_bytes;
     static constexpr int kq_off = 0, t_off = 0;
     static constexpr int m_off = (big + 1023) / 1024 * 1024;
     static_assert(m_off >= kq_bytes && m_off >= 2 * t_bytes, "k and q, and the operand rows, fit below M");
@@ -334,33 +333,18 @@ __device__ __forceinline__ void warp_matmul(float (&d)[MT][4], const float* A, i
         }
     }
 }
-// 8 columns of the lower left block of a block triangle's inverse: W = R P^-1
-// (kept in `work`, ld 12), then -Q^-1 W, R, P^-1 and Q^-1 each 16 MT square
-template <int MT>
-__device__ __forceinline__ void inverse_columns(const float* R, const float* Pinv, const float* Qinv, int ld, float* work,
-                                                float* out, int lane) {
+// A 16 x 8 tile to fp32 row-major shared memory, times `sign`
+__device__ __forceinline__ void store_tile(float* out, int ld, const float (&d)[4], float sign, int lane) {
     const int g = lane >> 2, c = lane & 3;
-    float d[MT][4];
-    warp_matmul<MT, 2 * MT>(d, R, ld, Pinv, ld, lane);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        *reinterpret_cast<float2*>(work + (16 * m + g) * 12 + 2 * c) = f2(d[m][0], d[m][1]);
-        *reinterpret_cast<float2*>(work + (16 * m + g + 8) * 12 + 2 * c) = f2(d[m][2], d[m][3]);
-    }
-    __syncwarp();
-    warp_matmul<MT, 2 * MT>(d, Qinv, ld, work, 12, lane);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        *reinterpret_cast<float2*>(out + (16 * m + g) * ld + 2 * c) = f2(-d[m][0], -d[m][1]);
-        *reinterpret_cast<float2*>(out + (16 * m + g + 8) * ld + 2 * c) = f2(-d[m][2], -d[m][3]);
-    }
+    *reinterpret_cast<float2*>(out + g * ld + 2 * c) = f2(sign * d[0], sign * d[1]);
+    *reinterpret_cast<float2*>(out + (g + 8) * ld + 2 * c) = f2(sign * d[2], sign * d[3]);
 }
 
 // Eight warps.  Warp w reaches the tensor-memory lanes of quarter w % 4: rows
 // 32 (w % 4).. of [k; q] [k; q]^T, whose diagonal holds the norms and whose
 // columns of k, 32 (w / 4).. for this warp, become L (quarters 0 and 1) and M.
 template <int N>
-__global__ void __launch_bounds__(kGdrPrepThreads, 3)
+__global__ void __launch_bounds__(kGdrPrepThreads, 4)
 gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_t)
 {
@@ -371,7 +355,6 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     unsigned char* kq = sm + Lay::kq_off;
     float* Lm = reinterpret_cast<float*>(sm + Lay::l_off);
     float* Tm = reinterpret_cast<float*>(sm + Lay::inv_off);
-    float* Wm = reinterpret_cast<float*>(sm + Lay::work_off);
     unsigned char* mt = sm + Lay::m_off;                 // M hi, lo: 64 rows each
     unsigned char* tt = sm + Lay::t_off;                 // [T; M T] hi, lo: 128 rows each
     float* cum_hi = reinterpret_cast<float*>(sm + Lay::f_off);   // prefix sums times log2(e), hi + lo
@@ -391,7 +374,7 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     const int g = h / (p.H / p.G);
     if (p.status && tid == 0 && c == 0 && h == 0 && b == 0) p.status[1] = p.status_epoch;
 
-    if (tid == 0) {
+    if (tid == 7 * 32) {
         mbar_init(&bars[0], 1);
         mbar_init(&bars[1], 1);
         mbar_init(&bars[2], 1);
@@ -543,14 +526,27 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         for (int j = (i / 16 + 1) * 16; j < kGdrC; j += 4) *reinterpret_cast<float4*>(Tm + i * ld + j) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     __syncthreads();
+    // W lies in L's upper right block, which nothing reads
     if (warp < 4) {
         const int o = (warp >> 1) * 32, n = (warp & 1) * 8;
-        inverse_columns<1>(Lm + (o + 16) * ld + o, Tm + o * ld + o + n, Tm + (o + 16) * ld + o + 16, ld, Wm + warp * 32 * 12,
-                           Tm + (o + 16) * ld + o + n, lane);
+        float* work = Lm + o / 2 * ld + 32 + n;
+        float d[1][4];
+        warp_matmul<1, 2>(d, Lm + (o + 16) * ld + o, ld, Tm + o * ld + o + n, ld, lane);
+        store_tile(work, ld, d[0], 1.0f, lane);
+        __syncwarp();
+        warp_matmul<1, 2>(d, Tm + (o + 16) * ld + o + 16, ld, work, ld, lane);
+        store_tile(Tm + (o + 16) * ld + o + n, ld, d[0], -1.0f, lane);
     }
     __syncthreads();
-    if (warp < 4)
-        inverse_columns<2>(Lm + 32 * ld, Tm + warp * 8, Tm + 32 * ld + 32, ld, Wm + warp * 32 * 12, Tm + 32 * ld + warp * 8, lane);
+    {
+        const int n = (warp & 3) * 8, m = (warp >> 2) * 16;
+        float d[1][4];
+        warp_matmul<1, 4>(d, Lm + (32 + m) * ld, ld, Tm + n, ld, lane);
+        store_tile(Lm + m * ld + 32 + n, ld, d[0], 1.0f, lane);
+        __syncthreads();
+        warp_matmul<1, 4>(d, Tm + (32 + m) * ld + 32, ld, Lm + 32 + n, ld, lane);
+        store_tile(Tm + (32 + m) * ld + n, ld, d[0], -1.0f, lane);
+    }
     __syncthreads();
     // T diag(b), split, as rows 0..63 of the operand tile
     {
@@ -601,12 +597,17 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         }
         fence_proxy_async_smem();
     }
+    tc_fence_before();
     if (__syncthreads_and(done)) {
         if (tid == 0) {
             tma_store_2d(&tm_t, tt, 0, static_cast<int>(unit * 256));
             tma_store_2d(&tm_t, tt + Lay::t_bytes, 0, static_cast<int>(unit * 256 + 128));
             bulk_commit_group();
             bulk_wait_read_all();
+        }
+        if (warp == 2) {
+            tc_fence_after();
+            tmem_dealloc(tmem, 128);
         }
     } else {
         if (tid == 0) gdr_fail(p);
@@ -615,12 +616,8 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
             if (!loaded) mbar_wait_bounded(&bars[0], 0, 1u << 20);
             else mbar_wait_bounded(&bars[ready ? 2 : 1], 0, 1u << 20);
         }
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 2) {
-        tc_fence_after();
-        tmem_dealloc(tmem, 128);
+        __syncthreads();
+        if (warp == 2) tmem_dealloc(tmem, 128);
     }
 }
 
