@@ -238,6 +238,9 @@ struct GdrChunkParams {
     int64_t L;
     int H, G, P;
     int chunk0, chunks;           // this launch's chunks of the sequence
+    int segs, seg_chunks;         // its segments, and their chunks (the last may have fewer)
+    float* seg_out;               // [B][segs - 1][H][P + N][N] a segment's last state from zero, then its transition
+    float* seg_in;                // [B][segs - 1][H][P][N] the state that enters segment 1, 2, ..
     float scale, eps;
     unsigned wait_limit;
     unsigned long long* status;
@@ -600,8 +603,8 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     tc_fence_before();
     if (__syncthreads_and(done)) {
         if (tid == 0) {
-            tma_store_2d(&tm_t, tt, 0, static_cast<int>(unit * 256));
-            tma_store_2d(&tm_t, tt + Lay::t_bytes, 0, static_cast<int>(unit * 256 + 128));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tma_store_2d(&tm_t, tt + k * 8192, 0, static_cast<int>(unit * 256 + k * 64));
             bulk_commit_group();
             bulk_wait_read_all();
         }
@@ -685,7 +688,11 @@ __device__ __forceinline__ void tmem_ld_sum(uint32_t taddr, float (&v)[COLS]) {
 // 2 and 3 their queries (y).  With N = 64 product 3 takes the 64 rows of k^T
 // twice (both 64-row blocks of the operand at one address), so that all four
 // quarters hold the state, 8 columns a thread instead of 16.
-template <int N>
+//
+// STATE: the pass over segments before the one that writes y (see
+// gdr_segment_kernel).  A tile of P / 64 or above is one of the transition's:
+// its rows start as rows of the identity and its v is zero.
+template <int N, bool STATE>
 __global__ void __launch_bounds__(kGdrScanThreads, 1)
 gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_t)
@@ -705,9 +712,14 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + 3);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int tile = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int segs = STATE ? p.segs - 1 : p.segs;
+    const int tile = blockIdx.x, h = blockIdx.y, b = blockIdx.z / segs, seg = blockIdx.z - b * segs;
     const int g = h / (p.H / p.G);
-    const int n_chunks = p.chunks;
+    const int first = seg * p.seg_chunks;
+    const int n_chunks = min(p.seg_chunks, p.chunks - first);
+    const bool values = tile < p.P / kGdrTile;
+    if (STATE && !values && seg == 0) return;      // the first segment's own state is known
+    constexpr uint32_t t_rows = STATE ? 64 : 128;  // of [T; M T], and [k; q], that this pass uses
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -740,22 +752,23 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 const unsigned par = static_cast<unsigned>(((c / kStages) & 1) ^ 1);
                 unsigned char* kq = sm + s * Lay::in_bytes;
                 unsigned char* tt = sm + Lay::t_off + s * 2 * Lay::t_bytes;
-                const int tok = (p.chunk0 + c) * kGdrC;
+                const int tok = (p.chunk0 + first + c) * kGdrC;
                 if (!(ok = mbar_wait_bounded(&kq_free[s], par, p.wait_limit))) break;
-                const int64_t unit = (static_cast<int64_t>(b) * p.chunks + c) * p.H + h;
-                mbar_arrive_expect_tx(&kq_full[s], Lay::in_bytes);
+                const int64_t unit = (static_cast<int64_t>(b) * p.chunks + first + c) * p.H + h;
+                mbar_arrive_expect_tx(&kq_full[s], t_rows * N * 2 + (values ? kGdrC * 128 : 0) + kGdrC * 16);
                 for (int kb = 0; kb < N / 64; ++kb) {
                     tma_load_3d(kq + kb * 16384, &tm_k, g * N + kb * 64, tok, b, &kq_full[s]);
-                    tma_load_3d(kq + kb * 16384 + 8192, &tm_q, g * N + kb * 64, tok, b, &kq_full[s]);
+                    if (!STATE) tma_load_3d(kq + kb * 16384 + 8192, &tm_q, g * N + kb * 64, tok, b, &kq_full[s]);
                 }
-                tma_load_3d(kq + Lay::v_off, &tm_v, h * p.P + tile * kGdrTile, tok, b, &kq_full[s]);
+                if (values) tma_load_3d(kq + Lay::v_off, &tm_v, h * p.P + tile * kGdrTile, tok, b, &kq_full[s]);
                 bulk_load(kq + Lay::fac_off, p.fac + unit * kGdrC, kGdrC * 16, &kq_full[s]);
                 ++issued;
                 if (!(ok = mbar_wait_bounded(&t_free[s], par, p.wait_limit))) break;
                 const int row = static_cast<int>(unit * 256);
-                mbar_arrive_expect_tx(&t_full[s], 2 * Lay::t_bytes);
-                tma_load_2d(tt, &tm_t, 0, row, &t_full[s]);
-                tma_load_2d(tt + Lay::t_bytes, &tm_t, 0, row + 128, &t_full[s]);
+                mbar_arrive_expect_tx(&t_full[s], 2 * t_rows * 128);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (!STATE || k % 2 == 0) tma_load_2d(tt + k * 8192, &tm_t, 0, row + k * 64, &t_full[s]);
                 ++issued;
             }
         }
@@ -817,15 +830,23 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         unsigned char* sp = sm + Lay::s_off;
         unsigned char* xp = sm + Lay::x_off;
         float S[kCols];
-        const int64_t state = ((static_cast<int64_t>(b) * p.H + h) * p.P + tile * kGdrTile + srow0) * N + n;
+        const int64_t heads = (static_cast<int64_t>(b) * p.H + h), row = tile * kGdrTile + srow0;
+        const int64_t state = (heads * p.P + row) * N + n;
+        // segment `seg_` of the P (or P + N) rows of a state of each but one
+        auto of_segment = [&](int seg_, int rows) {
+            return (((static_cast<int64_t>(b) * (p.segs - 1) + seg_) * p.H + h) * rows + row) * N + n;
+        };
+        const float* src = seg == 0 ? (p.h_in ? p.h_in + state : nullptr)
+                                    : (STATE ? nullptr : p.seg_in + of_segment(seg - 1, p.P));
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) S[j] = p.h_in ? p.h_in[state + static_cast<int64_t>(j) * N] : 0.0f;
+        for (int j = 0; j < kCols; ++j)
+            S[j] = src ? src[static_cast<int64_t>(j) * N] : (STATE && row + j == p.P + n ? 1.0f : 0.0f);
 
         // y of a chunk, stored once the next chunk's first operand is written:
         // the fence before that waits for the memory operations before it
         uint32_t yw[8];
         auto store_y = [&](int c) {
-            const int64_t t = static_cast<int64_t>(p.chunk0 + c) * kGdrC + i;
+            const int64_t t = static_cast<int64_t>(p.chunk0 + first + c) * kGdrC + i;
             if (t < p.L) {
                 uint4* dst = reinterpret_cast<uint4*>(p.y + ((static_cast<int64_t>(b) * p.L + t) * p.H + h) * p.P +
                                                       tile * kGdrTile + col0);
@@ -847,14 +868,15 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
             tc_fence_before();
             __syncwarp();
             if (elect_one_lane()) mbar_arrive(&in_full[0]);
-            if (q >= 2 && c > 0) store_y(c - 1);
+            if (!STATE && q >= 2 && c > 0) store_y(c - 1);
 
             if (!(ok = warp_wait(&kq_full[s], static_cast<unsigned>((c / kStages) & 1), p.wait_limit))) break;
             const float4 f = *reinterpret_cast<const float4*>(in + Lay::fac_off + i * 16);
             uint4 v[2];
             if (q < 2) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) v[k] = *reinterpret_cast<const uint4*>(in + Lay::v_off + sw128_off(i, wg * 2 + k));
+                for (int k = 0; k < 2; ++k) 
+                    v[k] = values ? *reinterpret_cast<const uint4*>(in + Lay::v_off + sw128_off(i, wg * 2 + k)) : make_uint4(0u, 0u, 0u, 0u);
             } else {
                 // no u' of this warp's: it only must have read its factors
                 // before product 3 lets the next chunk but one overwrite them
@@ -864,7 +886,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
             if (!(ok = warp_wait(&d_full[0], par, p.wait_limit))) break;
             tc_fence_after();
             float d[16];
-            tmem_ld_sum<16>(lane_base + kD1 + col0, d);
+            if (!STATE || q < 2) tmem_ld_sum<16>(lane_base + kD1 + col0, d);
             if (q < 2) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -886,7 +908,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
             if (!(ok = warp_wait(&d_full[1], par, p.wait_limit))) break;
             tc_fence_after();
             float u[16];
-            tmem_ld_sum<16>(lane_base + kD2 + col0, u);
+            if (!STATE || q < 2) tmem_ld_sum<16>(lane_base + kD2 + col0, u);
             if (q < 2) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -899,7 +921,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 tc_fence_before();
                 __syncwarp();
                 if (elect_one_lane()) mbar_arrive(&in_full[2]);
-            } else {
+            } else if (!STATE) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     yw[e] = pack_bf16x2(fmaf(f.z, d[2 * e], u[2 * e]), fmaf(f.z, d[2 * e + 1], u[2 * e + 1]));
@@ -911,10 +933,11 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
 #pragma unroll
             for (int j = 0; j < kCols; ++j) S[j] = fmaf(f.w, S[j], add[j]);
         }
-        if (ok && q >= 2) store_y(n_chunks - 1);
-        if (ok) {
+        if (!STATE && ok && q >= 2) store_y(n_chunks - 1);
+        if (ok && (STATE || seg == p.segs - 1)) {
+            float* dst = STATE ? p.seg_out + of_segment(seg, p.P + N) : p.h_out + state;
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) p.h_out[state + static_cast<int64_t>(j) * N] = S[j];
+            for (int j = 0; j < kCols; ++j) dst[static_cast<int64_t>(j) * N] = S[j];
         }
     }
     tc_fence_before();
@@ -935,6 +958,55 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     if (warp == kGdrWarps) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- segments of a long sequence
+// A chunk's products wait for one another, so a sequence's chunks in order
+// leave most SMs idle when there are few heads.  A segment of chunks is affine
+// in the state that enters it, S_out = S_in A + S_0, with S_0 its last state
+// from zero and row m of A its last state from row m of the identity without
+// values.  So: gdr_scan_kernel<N, true> over all segments but the last for
+// S_0 and A (N more rows of a state), this kernel for the states entering
+// them, in order, and gdr_scan_kernel<N, false> over all segments at once.
+// CTA: 8 rows of a head's state; thread: one column; fp32.
+constexpr int kGdrSegRows = 8;
+template <int N>
+__global__ void __launch_bounds__(N)
+gdr_segment_kernel(const GdrChunkParams p)
+{
+    __shared__ __align__(16) float cur[N][kGdrSegRows];
+    const int n = threadIdx.x, row0 = blockIdx.x * kGdrSegRows, h = blockIdx.y, b = blockIdx.z;
+    const int rows = p.P + N;
+    float s[kGdrSegRows];
+    for (int seg = 0; seg + 1 < p.segs; ++seg) {
+        const int64_t sh = (static_cast<int64_t>(b) * (p.segs - 1) + seg) * p.H + h;
+        const float* from = p.seg_out + (sh * rows + row0) * N + n;
+        float next[kGdrSegRows];
+#pragma unroll
+        for (int r = 0; r < kGdrSegRows; ++r) next[r] = from[r * N];
+        if (seg > 0) {
+#pragma unroll
+            for (int r = 0; r < kGdrSegRows; ++r) cur[n][r] = s[r];
+            __syncthreads();
+            const float* A = p.seg_out + (sh * rows + p.P) * N + n;
+#pragma unroll 16
+            for (int m = 0; m < N; ++m) {
+                const float a = A[m * N];
+#pragma unroll
+                for (int r = 0; r < kGdrSegRows; r += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(&cur[m][r]);
+                    next[r] = fmaf(v.x, a, next[r]);
+                    next[r + 1] = fmaf(v.y, a, next[r + 1]);
+                    next[r + 2] = fmaf(v.z, a, next[r + 2]);
+                    next[r + 3] = fmaf(v.w, a, next[r + 3]);
+                }
+            }
+            __syncthreads();
+        }
+        float* to = p.seg_in + (sh * p.P + row0) * N + n;
+#pragma unroll
+        for (int r = 0; r < kGdrSegRows; ++r) to[r * N] = s[r] = next[r];
     }
 }
 

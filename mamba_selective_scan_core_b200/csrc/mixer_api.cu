@@ -1963,15 +1963,38 @@ mm_status launch_gdr_recurrent(const mm::GdrParams& p, const GdrArgs& a, cudaStr
 // coordinates and strides fit (a workspace row index in 31 bits, a tensor's
 // strides in 40).  The chunks run in rounds of as many as bring the workspace
 // to kGdrRoundUnits chunks of a head, each round from the state that the one
-// before left in h_last.
+// before left in the workspace (two of them in turn: a round's first segment
+// reads one while its last writes the other).
 constexpr int64_t kGdrChunkedMin = 24;
 constexpr int64_t kGdrRoundUnits = 16384;      // 33 KB each
 struct GdrPlan {
     bool chunked = false;
     int64_t chunks = 0, round = 0;             // of a sequence; of a launch
-    size_t off_fac = 0, off_t = 0, total = kWsHeader;
+    int segs = 1;                              // of a launch's chunks, at most
+    size_t off_fac = 0, off_t = 0, off_out = 0, off_in = 0, off_carry = 0, total = kWsHeader;
 };
-GdrPlan plan_gdr(int64_t batch, int64_t seqlen, int64_t heads, mm_dtype act) {
+// Segments for `chunks` chunks: as many as make the passes over them shortest,
+// counting one step per chunk and wave of CTAs (one a SM).  The pass that
+// finds the segments' transitions has N / 64 more tiles a head, for all but
+// the last segment; a segment's place in the order costs about half a step (its
+// 128 x 128 product), and the two more launches about four.
+int gdr_segments(int64_t batch, int64_t tiles, int64_t trans_tiles, int64_t chunks, int64_t sms) {
+    int best = 1;
+    int64_t best_cost = 0;
+    for (int n = 1; n <= 32 && 4 * (n - 1) < chunks && n * batch <= 65535; ++n) {
+        const int64_t each = (chunks + n - 1) / n;
+        if ((n - 1) * each >= chunks) continue;           // fewer segments do
+        auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
+        const int64_t steps = waves(n * tiles) * each + (n > 1 ? waves((n - 1) * (tiles + trans_tiles)) * each : 0);
+        const int64_t cost = 2 * steps + (n > 1 ? n + 8 : 0);
+        if (n == 1 || cost < best_cost) {
+            best = n;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+GdrPlan plan_gdr(int64_t batch, int64_t seqlen, int64_t heads, int64_t headdim, int64_t d_state, mm_dtype act, int64_t sms) {
     GdrPlan pl;
     if (act != MM_BF16 || seqlen < kGdrChunkedMin || batch * heads > (int64_t(1) << 20)) return pl;
     pl.chunked = true;
@@ -1980,7 +2003,12 @@ GdrPlan plan_gdr(int64_t batch, int64_t seqlen, int64_t heads, mm_dtype act) {
     const int64_t units = batch * heads * pl.round;
     pl.off_fac = kWsHeader;
     pl.off_t = pl.off_fac + static_cast<size_t>(units) * mm::kGdrC * 16;
-    pl.total = pl.off_t + static_cast<size_t>(units) * 2 * (2 * mm::kGdrC * 128);
+    pl.off_out = pl.off_t + static_cast<size_t>(units) * 2 * (2 * mm::kGdrC * 128);
+    pl.segs = gdr_segments(batch, batch * heads * headdim / mm::kGdrTile, batch * heads * d_state / mm::kGdrTile, pl.round, sms);
+    const int64_t rows = batch * heads * (pl.segs - 1) * d_state;
+    pl.off_in = pl.off_out + static_cast<size_t>(rows * (headdim + d_state)) * 4;
+    pl.off_carry = pl.off_in + static_cast<size_t>(rows * headdim) * 4;
+    pl.total = pl.off_carry + (pl.round < pl.chunks ? static_cast<size_t>(batch * heads * headdim * d_state) * 8 : 0);
     return pl;
 }
 
@@ -2004,20 +2032,21 @@ mm_status launch_gdr_chunked(const GdrArgs& a, const GdrPlan& pl, unsigned char*
     if (!encode_gdr_rows(&tq, a.q, a.groups * N, a.q_stride, a.seqlen, a.batch) ||
         !encode_gdr_rows(&tk, a.k, a.groups * N, a.k_stride, a.seqlen, a.batch) ||
         !encode_gdr_rows(&tv, a.v, a.heads * a.headdim, a.v_stride, a.seqlen, a.batch) ||
-        !encode_gemm_2d(&tt, w + pl.off_t, 64, a.batch * a.heads * pl.round * 256, 128))
+        !encode_gemm_2d(&tt, w + pl.off_t, 64, a.batch * a.heads * pl.round * 256, 64))
         return MM_ERR_CUDA;
-    static std::atomic<unsigned long long> allowed_prep{0}, allowed_scan{0};
+    static std::atomic<unsigned long long> allowed_prep{0}, allowed_scan{0}, allowed_state{0};
     if (allow_smem(mm::gdr_prep_kernel<N>, allowed_prep) != cudaSuccess ||
-        allow_smem(mm::gdr_scan_kernel<N>, allowed_scan) != cudaSuccess) { cudaGetLastError(); return MM_ERR_CUDA; }
+        allow_smem(mm::gdr_scan_kernel<N, false>, allowed_scan) != cudaSuccess ||
+        allow_smem(mm::gdr_scan_kernel<N, true>, allowed_state) != cudaSuccess) { cudaGetLastError(); return MM_ERR_CUDA; }
     mm::GdrChunkParams p{};
     p.dt = static_cast<const __nv_bfloat16*>(a.dt);
     p.beta = static_cast<const __nv_bfloat16*>(a.beta);
     p.dt_bias = a.dt_bias;
     p.A = a.A;
-    p.h_in = a.h0;
     p.y = static_cast<__nv_bfloat16*>(a.y);
-    p.h_out = a.h_last;
     p.fac = reinterpret_cast<float4*>(w + pl.off_fac);
+    p.seg_out = reinterpret_cast<float*>(w + pl.off_out);
+    p.seg_in = reinterpret_cast<float*>(w + pl.off_in);
     p.L = a.seqlen;
     p.H = static_cast<int>(a.heads);
     p.G = static_cast<int>(a.groups);
@@ -2028,15 +2057,29 @@ mm_status launch_gdr_chunked(const GdrArgs& a, const GdrPlan& pl, unsigned char*
     p.status = reinterpret_cast<unsigned long long*>(w);
     p.status_epoch = epoch;
     const bool fail = forced_launch_failure();
-    for (int64_t c0 = 0; c0 < pl.chunks; c0 += pl.round) {
+    float* carry = reinterpret_cast<float*>(w + pl.off_carry);
+    const int64_t state = a.batch * a.heads * a.headdim * N;
+    for (int64_t c0 = 0, r = 0; c0 < pl.chunks; c0 += pl.round, ++r) {
         p.chunk0 = static_cast<int>(c0);
         p.chunks = static_cast<int>(std::min(pl.round, pl.chunks - c0));
-        if (c0 > 0) p.h_in = a.h_last;
+        p.h_in = r == 0 ? a.h0 : carry + (r - 1) % 2 * state;
+        p.h_out = c0 + pl.round >= pl.chunks ? a.h_last : carry + r % 2 * state;
         mm::gdr_prep_kernel<N><<<dim3(static_cast<unsigned>(p.chunks), static_cast<unsigned>(p.H), static_cast<unsigned>(a.batch)),
                                  mm::kGdrPrepThreads, fail ? (1 << 20) : mm::GdrPrepLayout<N>::smem_bytes, s>>>(p, tq, tk, tt);
         if (cudaGetLastError() != cudaSuccess) return MM_ERR_CUDA;
-        mm::gdr_scan_kernel<N><<<dim3(static_cast<unsigned>(p.P / mm::kGdrTile), static_cast<unsigned>(p.H), static_cast<unsigned>(a.batch)),
-                                 mm::kGdrScanThreads, fail ? (1 << 20) : mm::GdrScanLayout<N>::smem_bytes, s>>>(p, tq, tk, tv, tt);
+        const int64_t each = (p.chunks + pl.segs - 1) / pl.segs;
+        p.seg_chunks = static_cast<int>(each);
+        p.segs = static_cast<int>((p.chunks + each - 1) / each);      // the last round may have fewer
+        const unsigned tiles = static_cast<unsigned>(p.P / mm::kGdrTile), smem = fail ? (1 << 20) : mm::GdrScanLayout<N>::smem_bytes;
+        const unsigned heads = static_cast<unsigned>(p.H), batch = static_cast<unsigned>(a.batch);
+        if (p.segs > 1) {
+            mm::gdr_scan_kernel<N, true><<<dim3(tiles + N / mm::kGdrTile, heads, batch * (p.segs - 1)), mm::kGdrScanThreads, smem,
+                                           s>>>(p, tq, tk, tv, tt);
+            if (cudaGetLastError() != cudaSuccess) return MM_ERR_CUDA;
+            mm::gdr_segment_kernel<N><<<dim3(static_cast<unsigned>(p.P / mm::kGdrSegRows), heads, batch), N, 0, s>>>(p);
+            if (cudaGetLastError() != cudaSuccess) return MM_ERR_CUDA;
+        }
+        mm::gdr_scan_kernel<N, false><<<dim3(tiles, heads, batch * p.segs), mm::kGdrScanThreads, smem, s>>>(p, tq, tk, tv, tt);
         if (cudaGetLastError() != cudaSuccess) return MM_ERR_CUDA;
     }
     return MM_OK;
@@ -2051,7 +2094,7 @@ size_t mamba_gdr_workspace_size(int64_t batch, int64_t seqlen, int64_t heads, in
     if ((act != MM_F32 && act != MM_BF16) || batch <= 0 || !gdr_sizes_ok(batch, seqlen, groups, heads) ||
         !gdr_supported(headdim, d_state))
         return 0;
-    return plan_gdr(batch, seqlen, heads, act).total;
+    return plan_gdr(batch, seqlen, heads, headdim, d_state, act, plan_sms()).total;
 }
 
 mm_status mamba_gdr_fwd(const void* q, const void* k, const void* v, const void* dt, const void* beta,
@@ -2065,7 +2108,7 @@ mm_status mamba_gdr_fwd(const void* q, const void* k, const void* v, const void*
     Span ins[8], outs[2];
     if (mm_status st = validate_gdr(a, false, ins, outs); st != MM_OK) return st;
     if (batch == 0) return MM_OK;
-    const GdrPlan pl = plan_gdr(batch, seqlen, heads, act);
+    const GdrPlan pl = plan_gdr(batch, seqlen, heads, headdim, d_state, act, plan_sms());
     const size_t need = pl.total;
     if (!workspace || workspace_bytes < need) return MM_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MM_ERR_ALIGN;

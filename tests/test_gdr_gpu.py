@@ -135,6 +135,41 @@ def test_padded_batch(L):
         close(h[b:b + 1], rh, "h_last")
 
 
+@pytest.mark.parametrize("B,L,G,H,P,N", [(1, 2500, 1, 1, 64, 64), (1, 2049, 1, 2, 192, 128), (2, 1600, 1, 2, 128, 64),
+                                         (1, 1985, 2, 2, 256, 128)])
+@pytest.mark.parametrize("dt_mean", [0.0, -8.0])
+def test_long_sequences_of_few_heads(B, L, G, H, P, N, dt_mean):
+    """Sequences whose chunks run in segments at once, each from the state that
+    the transitions of those before it give."""
+    check(gdr_inputs(B, L, G, H, P, N, seed=L, dt_mean=dt_mean, h0=B == 1))
+
+
+def test_more_chunks_than_one_round():
+    """A batch whose chunks' workspace is kept for part of the sequence at a
+    time: as two calls, the second from the first one's state."""
+    B, L, H, P, N, cut = 8, 64 * 130 + 5, 16, 64, 64, 4096
+    g = torch.Generator(device="cuda").manual_seed(97)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(BF)
+
+    d = {"q": normal(B, L, 1, N), "k": normal(B, L, 1, N), "v": normal(B, L, H, P), "dt": normal(B, L, H) - 4,
+         "beta": normal(B, L, H), "dt_bias": None, "A": -torch.ones(H, device="cuda"), "h0": None}
+    y, h = fwd(d)
+
+    def part(lo, hi, h0):
+        return {n: t if n == "A" or t is None else t[:, lo:hi].contiguous() for n, t in d.items() if n != "h0"} | {"h0": h0}
+
+    y1, h1 = fwd(part(0, cut, None))
+    y2, h2 = fwd(part(cut, L, h1))
+    torch.cuda.synchronize()
+    # both are within NORM of the exact values, and the rounded y within its last bit
+    assert (h - h2).norm() <= 2 * NORM * h.norm()
+    ref = torch.cat([y1, y2], 1).double()
+    err = ((y.double() - ref).abs() - 2.0 ** -7 * ref.abs()).clamp_min(0)
+    assert err.norm() <= 2 * NORM * ref.norm()
+
+
 @pytest.mark.parametrize("L", [40, 130])
 def test_all_tokens_masked(L):
     """A sequence of padding alone: the state comes back bit for bit."""
