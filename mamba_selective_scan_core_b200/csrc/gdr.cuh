@@ -252,13 +252,21 @@ __device__ __forceinline__ void gdr_fail(const GdrChunkParams& p) {
     if (p.status) atomicExch(p.status, (p.status_epoch << 8) | 1ull);
 }
 
+// two floats at a time (add, multiply and fma take a pair per instruction)
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+// (v.x, v.y) = hi + lo as split_bf16x2
+__device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16x2(v.x, v.y);
+    const float2 r = fma2(f2(bf16_lo(hi), bf16_hi(hi)), f2(-1.0f, -1.0f), v);
+    lo = pack_bf16x2(r.x, r.y);
+}
 // v[8] -> one 16-byte piece of each part
 __device__ __forceinline__ void split_store8(const float* v, unsigned char* hi_p, unsigned char* lo_p) {
     uint4 hi, lo;
-    split_bf16x2(v[0], v[1], hi.x, lo.x);
-    split_bf16x2(v[2], v[3], hi.y, lo.y);
-    split_bf16x2(v[4], v[5], hi.z, lo.z);
-    split_bf16x2(v[6], v[7], hi.w, lo.w);
+    split2(f2(v[0], v[1]), hi.x, lo.x);
+    split2(f2(v[2], v[3]), hi.y, lo.y);
+    split2(f2(v[4], v[5]), hi.z, lo.z);
+    split2(f2(v[6], v[7]), hi.w, lo.w);
     *reinterpret_cast<uint4*>(hi_p) = hi;
     *reinterpret_cast<uint4*>(lo_p) = lo;
 }
@@ -680,7 +688,12 @@ __device__ __forceinline__ void tmem_ld_sum(uint32_t taddr, float (&v)[COLS]) {
     }
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < COLS; ++i) v[i] = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
+    for (int i = 0; i < COLS; i += 2) {
+        const float2 r = add2(f2(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
+                              f2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
+        v[i] = r.x;
+        v[i + 1] = r.y;
+    }
 }
 // 16 elementwise warps, one that issues the products and one that copies.
 // Warp w reaches the tensor-memory lanes of quarter w % 4 and takes columns
@@ -842,98 +855,125 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         for (int j = 0; j < kCols; ++j)
             S[j] = src ? src[static_cast<int64_t>(j) * N] : (STATE && row + j == p.P + n ? 1.0f : 0.0f);
 
-        // y of a chunk, stored once the next chunk's first operand is written:
-        // the fence before that waits for the memory operations before it
-        uint32_t yw[8];
-        auto store_y = [&](int c) {
-            const int64_t t = static_cast<int64_t>(p.chunk0 + first + c) * kGdrC + i;
-            if (t < p.L) {
-                uint4* dst = reinterpret_cast<uint4*>(p.y + ((static_cast<int64_t>(b) * p.L + t) * p.H + h) * p.P +
-                                                      tile * kGdrTile + col0);
-                dst[0] = make_uint4(yw[0], yw[1], yw[2], yw[3]);
-                dst[1] = make_uint4(yw[4], yw[5], yw[6], yw[7]);
-            }
+        auto wait = [&](uint64_t* bar, unsigned parity) { return ok = warp_wait(bar, parity, p.wait_limit); };
+        auto arrive = [&](uint64_t* bar) {
+            __syncwarp();
+            if (elect_one_lane()) mbar_arrive(bar);
         };
-        for (int c = 0; c < n_chunks; ++c) {
-            const int s = c % kStages;
-            const unsigned par = static_cast<unsigned>(c & 1);
-            const unsigned char* in = sm + s * Lay::in_bytes;
-            // S's parts, entry n of the tile's rows
+        // this thread's part of an operand is written: to the products
+        auto hand_over = [&](uint64_t* bar) {
+            fence_proxy_async_smem();
+            tc_fence_before();
+            arrive(bar);
+        };
+        auto write_state = [&] {
 #pragma unroll
             for (int k = 0; k < kCols / 8; ++k) {
                 const uint32_t off = sw128_off(n, srow0 / 8 + k);
                 split_store8(S + 8 * k, sp + off, sp + Lay::s_bytes + off);
             }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (elect_one_lane()) mbar_arrive(&in_full[0]);
-            if (!STATE && q >= 2 && c > 0) store_y(c - 1);
-
-            if (!(ok = warp_wait(&kq_full[s], static_cast<unsigned>((c / kStages) & 1), p.wait_limit))) break;
-            const float4 f = *reinterpret_cast<const float4*>(in + Lay::fac_off + i * 16);
-            uint4 v[2];
-            if (q < 2) {
+            hand_over(&in_full[0]);
+        };
+        auto add_state = [&](float decay) {
+            float add[kCols];
+            tmem_ld_sum<kCols>(lane_base + kD3 + srow0, add);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) 
-                    v[k] = values ? *reinterpret_cast<const uint4*>(in + Lay::v_off + sw128_off(i, wg * 2 + k)) : make_uint4(0u, 0u, 0u, 0u);
-            } else {
-                // no u' of this warp's: it only must have read its factors
-                // before product 3 lets the next chunk but one overwrite them
-                __syncwarp();
-                if (elect_one_lane()) mbar_arrive(&in_full[2]);
+            for (int j = 0; j < kCols; j += 2) {
+                const float2 r = fma2(f2(decay, decay), f2(S[j], S[j + 1]), f2(add[j], add[j + 1]));
+                S[j] = r.x;
+                S[j + 1] = r.y;
             }
-            if (!(ok = warp_wait(&d_full[0], par, p.wait_limit))) break;
-            tc_fence_after();
-            float d[16];
-            if (!STATE || q < 2) tmem_ld_sum<16>(lane_base + kD1 + col0, d);
-            if (q < 2) {
+        };
+        if (q < 2) {
+            for (int c = 0; c < n_chunks; ++c) {
+                const int s = c % kStages;
+                const unsigned par = static_cast<unsigned>(c & 1);
+                const unsigned char* in = sm + s * Lay::in_bytes;
+                write_state();
+                if (!wait(&kq_full[s], static_cast<unsigned>((c / kStages) & 1))) break;
+                const float4 f = *reinterpret_cast<const float4*>(in + Lay::fac_off + i * 16);
+                uint4 v[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    v[k] = values ? *reinterpret_cast<const uint4*>(in + Lay::v_off + sw128_off(i, wg * 2 + k)) : make_uint4(0u, 0u, 0u, 0u);
+                if (!wait(&d_full[0], par)) break;
+                tc_fence_after();
+                float x[16];
+                tmem_ld_sum<16>(lane_base + kD1 + col0, x);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t off = sw128_off(i, wg * 2 + k);
                     const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-                    float x[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        x[2 * e] = fmaf(-f.x, d[8 * k + 2 * e], bf16_lo(w[e]));
-                        x[2 * e + 1] = fmaf(-f.x, d[8 * k + 2 * e + 1], bf16_hi(w[e]));
+                        const float2 r = fma2(f2(-f.x, -f.x), f2(x[8 * k + 2 * e], x[8 * k + 2 * e + 1]), f2(bf16_lo(w[e]), bf16_hi(w[e])));
+                        x[8 * k + 2 * e] = r.x;
+                        x[8 * k + 2 * e + 1] = r.y;
                     }
-                    split_store8(x, xp + off, xp + Lay::x_bytes + off);
+                    split_store8(x + 8 * k, xp + off, xp + Lay::x_bytes + off);
                 }
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (elect_one_lane()) mbar_arrive(&in_full[1]);
-            }
-            if (!(ok = warp_wait(&d_full[1], par, p.wait_limit))) break;
-            tc_fence_after();
-            float u[16];
-            if (!STATE || q < 2) tmem_ld_sum<16>(lane_base + kD2 + col0, u);
-            if (q < 2) {
+                hand_over(&in_full[1]);
+                if (!wait(&d_full[1], par)) break;
+                tc_fence_after();
+                float u[16];
+                tmem_ld_sum<16>(lane_base + kD2 + col0, u);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) u[8 * k + e] *= f.y;
                     const uint32_t off = sw128_off(i, wg * 2 + k);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const float2 r = mul2(f2(f.y, f.y), f2(u[8 * k + e], u[8 * k + e + 1]));
+                        u[8 * k + e] = r.x;
+                        u[8 * k + e + 1] = r.y;
+                    }
                     split_store8(u + 8 * k, xp + off, xp + Lay::x_bytes + off);
                 }
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (elect_one_lane()) mbar_arrive(&in_full[2]);
-            } else if (!STATE) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    yw[e] = pack_bf16x2(fmaf(f.z, d[2 * e], u[2 * e]), fmaf(f.z, d[2 * e + 1], u[2 * e + 1]));
+                hand_over(&in_full[2]);
+                if (!wait(&d_full[2], par)) break;
+                tc_fence_after();
+                add_state(f.w);
             }
-            if (!(ok = warp_wait(&d_full[2], par, p.wait_limit))) break;
-            tc_fence_after();
-            float add[kCols];
-            tmem_ld_sum<kCols>(lane_base + kD3 + srow0, add);
+        } else {
+            // y of a chunk, stored once the next chunk's first operand is
+            // written: the fence before that waits for the memory operations before it
+            uint32_t yw[8] = {};
+            auto store_y = [&](int c) {
+                const int64_t t = static_cast<int64_t>(p.chunk0 + first + c) * kGdrC + i;
+                if (t < p.L) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.y + ((static_cast<int64_t>(b) * p.L + t) * p.H + h) * p.P +
+                                                          tile * kGdrTile + col0);
+                    dst[0] = make_uint4(yw[0], yw[1], yw[2], yw[3]);
+                    dst[1] = make_uint4(yw[4], yw[5], yw[6], yw[7]);
+                }
+            };
+            for (int c = 0; c < n_chunks; ++c) {
+                const int s = c % kStages;
+                const unsigned par = static_cast<unsigned>(c & 1);
+                write_state();
+                if (!STATE && c > 0) store_y(c - 1);
+                if (!wait(&kq_full[s], static_cast<unsigned>((c / kStages) & 1))) break;
+                const float4 f = *reinterpret_cast<const float4*>(sm + s * Lay::in_bytes + Lay::fac_off + i * 16);
+                // no u' of this warp's: it only must have read its factors
+                // before product 3 lets the next chunk but one overwrite them
+                arrive(&in_full[2]);
+                if (!STATE) {
+                    if (!wait(&d_full[1], par)) break;
+                    tc_fence_after();
+                    float d[16], u[16];
+                    tmem_ld_sum<16>(lane_base + kD1 + col0, d);
+                    tmem_ld_sum<16>(lane_base + kD2 + col0, u);
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) S[j] = fmaf(f.w, S[j], add[j]);
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 r = fma2(f2(f.z, f.z), f2(d[2 * e], d[2 * e + 1]), f2(u[2 * e], u[2 * e + 1]));
+                        yw[e] = pack_bf16x2(r.x, r.y);
+                    }
+                }
+                if (!wait(&d_full[2], par)) break;
+                tc_fence_after();
+                add_state(f.w);
+            }
+            if (!STATE && ok) store_y(n_chunks - 1);
         }
-        if (!STATE && ok && q >= 2) store_y(n_chunks - 1);
         if (ok && (STATE || seg == p.segs - 1)) {
             float* dst = STATE ? p.seg_out + of_segment(seg, p.P + N) : p.h_out + state;
 #pragma unroll
@@ -969,28 +1009,64 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
 // values.  So: gdr_scan_kernel<N, true> over all segments but the last for
 // S_0 and A (N more rows of a state), this kernel for the states entering
 // them, in order, and gdr_scan_kernel<N, false> over all segments at once.
-// CTA: 8 rows of a head's state; thread: one column; fp32.
-constexpr int kGdrSegRows = 8;
+// CTA: 16 rows of a head's state; thread: one column; fp32, 128 x 128 x 16 a
+// segment from A in shared memory, the next segment's on its way meanwhile
+// (read from L2 by each thread, it took 18 us a segment).
+constexpr int kGdrSegRows = 16;
+template <int N>
+struct GdrSegmentLayout {
+    static constexpr int a_bytes = N * N * 4;
+    static constexpr int cur_off = 2 * a_bytes;
+    static constexpr int bar_off = cur_off + N * kGdrSegRows * 4;
+    static constexpr int smem_bytes = bar_off + 16;
+};
 template <int N>
 __global__ void __launch_bounds__(N)
 gdr_segment_kernel(const GdrChunkParams p)
 {
-    __shared__ __align__(16) float cur[N][kGdrSegRows];
+    using Lay = GdrSegmentLayout<N>;
+    extern __shared__ __align__(128) unsigned char gdt_sm[];
+    float (*cur)[kGdrSegRows] = reinterpret_cast<float (*)[kGdrSegRows]>(gdt_sm + Lay::cur_off);
+    uint64_t* full = reinterpret_cast<uint64_t*>(gdt_sm + Lay::bar_off);      // A's two buffers
     const int n = threadIdx.x, row0 = blockIdx.x * kGdrSegRows, h = blockIdx.y, b = blockIdx.z;
     const int rows = p.P + N;
+    auto at = [&](int seg) { return (static_cast<int64_t>(b) * (p.segs - 1) + seg) * p.H + h; };
+    auto request = [&](int seg) {
+        mbar_arrive_expect_tx(&full[seg & 1], Lay::a_bytes);
+        bulk_load(gdt_sm + (seg & 1) * Lay::a_bytes, p.seg_out + (at(seg) * rows + p.P) * N, Lay::a_bytes, &full[seg & 1]);
+    };
+    if (n == 0) {
+        mbar_init(&full[0], 1);
+        mbar_init(&full[1], 1);
+        fence_mbar_init();
+        if (p.segs > 2) request(1);
+    }
+    __syncthreads();
     float s[kGdrSegRows];
     for (int seg = 0; seg + 1 < p.segs; ++seg) {
-        const int64_t sh = (static_cast<int64_t>(b) * (p.segs - 1) + seg) * p.H + h;
-        const float* from = p.seg_out + (sh * rows + row0) * N + n;
+        const float* from = p.seg_out + (at(seg) * rows + row0) * N + n;
         float next[kGdrSegRows];
 #pragma unroll
         for (int r = 0; r < kGdrSegRows; ++r) next[r] = from[r * N];
         if (seg > 0) {
+            // the buffer of the segment before is free: every thread is past it
+            if (n == 0 && seg + 2 < p.segs) request(seg + 1);
 #pragma unroll
             for (int r = 0; r < kGdrSegRows; ++r) cur[n][r] = s[r];
-            __syncthreads();
-            const float* A = p.seg_out + (sh * rows + p.P) * N + n;
-#pragma unroll 16
+            // buffer seg & 1 is filled for segments 1, 3, .. or 2, 4, ..
+            if (!__syncthreads_and(mbar_wait_bounded(&full[seg & 1], static_cast<unsigned>((seg - 1) >> 1) & 1u, p.wait_limit))) {
+                if (n == 0) {
+                    gdr_fail(p);
+                    // the copies in flight finish before their shared memory goes away
+                    mbar_wait_bounded(&full[seg & 1], static_cast<unsigned>((seg - 1) >> 1) & 1u, 1u << 20);
+                    if (seg + 2 < p.segs)
+                        mbar_wait_bounded(&full[(seg + 1) & 1], static_cast<unsigned>(seg >> 1) & 1u, 1u << 20);
+                }
+                __syncthreads();
+                return;
+            }
+            const float* A = reinterpret_cast<const float*>(gdt_sm + (seg & 1) * Lay::a_bytes) + n;
+#pragma unroll 8
             for (int m = 0; m < N; ++m) {
                 const float a = A[m * N];
 #pragma unroll
@@ -1004,7 +1080,7 @@ gdr_segment_kernel(const GdrChunkParams p)
             }
             __syncthreads();
         }
-        float* to = p.seg_in + (sh * p.P + row0) * N + n;
+        float* to = p.seg_in + (at(seg) * p.P + row0) * N + n;
 #pragma unroll
         for (int r = 0; r < kGdrSegRows; ++r) to[r * N] = s[r] = next[r];
     }

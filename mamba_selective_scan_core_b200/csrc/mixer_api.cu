@@ -2034,10 +2034,11 @@ mm_status launch_gdr_chunked(const GdrArgs& a, const GdrPlan& pl, unsigned char*
         !encode_gdr_rows(&tv, a.v, a.heads * a.headdim, a.v_stride, a.seqlen, a.batch) ||
         !encode_gemm_2d(&tt, w + pl.off_t, 64, a.batch * a.heads * pl.round * 256, 64))
         return MM_ERR_CUDA;
-    static std::atomic<unsigned long long> allowed_prep{0}, allowed_scan{0}, allowed_state{0};
+    static std::atomic<unsigned long long> allowed_prep{0}, allowed_scan{0}, allowed_state{0}, allowed_segment{0};
     if (allow_smem(mm::gdr_prep_kernel<N>, allowed_prep) != cudaSuccess ||
         allow_smem(mm::gdr_scan_kernel<N, false>, allowed_scan) != cudaSuccess ||
-        allow_smem(mm::gdr_scan_kernel<N, true>, allowed_state) != cudaSuccess) { cudaGetLastError(); return MM_ERR_CUDA; }
+        allow_smem(mm::gdr_scan_kernel<N, true>, allowed_state) != cudaSuccess ||
+        allow_smem(mm::gdr_segment_kernel<N>, allowed_segment) != cudaSuccess) { cudaGetLastError(); return MM_ERR_CUDA; }
     mm::GdrChunkParams p{};
     p.dt = static_cast<const __nv_bfloat16*>(a.dt);
     p.beta = static_cast<const __nv_bfloat16*>(a.beta);
@@ -2076,7 +2077,8 @@ mm_status launch_gdr_chunked(const GdrArgs& a, const GdrPlan& pl, unsigned char*
             mm::gdr_scan_kernel<N, true><<<dim3(tiles + N / mm::kGdrTile, heads, batch * (p.segs - 1)), mm::kGdrScanThreads, smem,
                                            s>>>(p, tq, tk, tv, tt);
             if (cudaGetLastError() != cudaSuccess) return MM_ERR_CUDA;
-            mm::gdr_segment_kernel<N><<<dim3(static_cast<unsigned>(p.P / mm::kGdrSegRows), heads, batch), N, 0, s>>>(p);
+            mm::gdr_segment_kernel<N><<<dim3(static_cast<unsigned>(p.P / mm::kGdrSegRows), heads, batch), N,
+                                        mm::GdrSegmentLayout<N>::smem_bytes, s>>>(p);
             if (cudaGetLastError() != cudaSuccess) return MM_ERR_CUDA;
         }
         mm::gdr_scan_kernel<N, false><<<dim3(tiles, heads, batch * p.segs), mm::kGdrScanThreads, smem, s>>>(p, tq, tk, tv, tt);
