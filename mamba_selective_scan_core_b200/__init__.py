@@ -807,24 +807,14 @@ def _check_rows(t, name, dtype, shape, device):
 
 
 # The calls below are made once per layer and decoded token, where a launch
-# takes a few microseconds: they look at each tensor with the fewest calls into
-# torch, and go through the checks that name what is wrong only once something is.
-def _fits(t, name, dtype, shape, dev, idx):
-    """_check, for a tensor that is given; idx is dev's index."""
-    if t.get_device() != idx or idx < 0 or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _check(t, name, dtype, shape, dev)
+# takes a few microseconds: one expression looks at all tensors with the fewest
+# calls into torch, and the checks that name what is wrong run once it fails.
+def _required(t, name):
+    if t is None:
+        raise ValueError(f"{name} must be given")
 
 
-def _row_stride(t, name, dtype, shape, dev, idx):
-    """_check_rows, whose common cases need no loop."""
-    if t.get_device() == idx >= 0 and t.dtype is dtype and t.shape == shape:
-        st = t.stride()
-        if st[-1] == 1 and st[-2] == shape[-1]:
-            if len(shape) == 3:
-                return st[0] if shape[0] > 1 else shape[1] * shape[2]
-            if shape[0] > 0 and shape[1] > 1 and st[0] == shape[1] * st[1]:
-                return st[1]
-    return _check_rows(t, name, dtype, shape, dev)
+_ERR_WORKSPACE = 9
 
 
 class _Torch:
@@ -835,7 +825,7 @@ class _Torch:
 
         self.f32, self.bf16, self.u8 = torch.float32, torch.bfloat16, torch.uint8
         self.codes = {torch.float32: MM_F32, torch.bfloat16: MM_BF16}
-        self.empty, self.device, self.current_device = torch.empty, torch.cuda.device, torch.cuda.current_device
+        self.device, self.current_device = torch.cuda.device, torch.cuda.current_device
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda i: torch.cuda.current_stream(i).cuda_stream)
         self.lib = lib()
@@ -849,14 +839,6 @@ def _names():
     if _torch_names is None:
         _torch_names = _Torch()
     return _torch_names
-
-
-def _call_on(T, dev, idx, fn, *args):
-    """fn(*args) with dev, whose index is idx, as the current device."""
-    if T.current_device() == idx:
-        return fn(*args)
-    with T.device(dev):
-        return fn(*args)
 
 
 def gdr_workspace_size(batch, seqlen, heads, headdim=128, d_state=128, groups=1, act=MM_BF16) -> int:
@@ -873,47 +855,72 @@ def gdr_fwd(q, k, v, dt, beta, dt_bias, A, h0=None, *, scale=None, norm_eps=1e-6
     when it is 0.  Returns (y [B,L,H,P], h_last [B,H,P,N] fp32), allocating any
     output not given."""
     T = _torch_names or _names()
-    f32, dtype = T.f32, v.dtype
+    f32, dtype, idx = T.f32, v.dtype, v.get_device()
     act = T.codes.get(dtype)
     if act is None:
         _act_code(dtype)
     Bsz, L, H, P = v.shape
     G, N = q.shape[2:]
-    dev, idx = v.device, v.get_device()
+    tokens, keys, state = (Bsz, L, H), (Bsz, L, G, N), (Bsz, H, P, N)
+    if not (idx >= 0 and q.dtype is dtype and k.dtype is dtype and q.get_device() == idx and k.get_device() == idx
+            and k.shape == keys and A is not None
+            and dt.shape == tokens and dt.dtype is dtype and dt.get_device() == idx and dt.is_contiguous()
+            and beta.shape == tokens and beta.dtype is dtype and beta.get_device() == idx and beta.is_contiguous()
+            and A.shape == (H,) and A.dtype is f32 and A.get_device() == idx and A.is_contiguous()
+            and (dt_bias is None or (dt_bias.shape == (H,) and dt_bias.dtype is f32 and dt_bias.get_device() == idx
+                                     and dt_bias.is_contiguous()))
+            and (h0 is None or (h0.shape == state and h0.dtype is f32 and h0.get_device() == idx and h0.is_contiguous()))
+            and (y is None or (y.shape == v.shape and y.dtype is dtype and y.get_device() == idx and y.is_contiguous()))
+            and (h_last is None or (h_last.shape == state and h_last.dtype is f32 and h_last.get_device() == idx
+                                    and h_last.is_contiguous()))):
+        dev = v.device
+        for t, name, want, shape in ((dt, "dt", dtype, tokens), (beta, "beta", dtype, tokens), (A, "A", f32, (H,))):
+            _required(t, name)
+            _check(t, name, want, shape, dev)
+        for t, name, want, shape in ((dt_bias, "dt_bias", f32, (H,)), (h0, "h0", f32, state), (y, "y", dtype, (Bsz, L, H, P)),
+                                     (h_last, "h_last", f32, state)):
+            _check(t, name, want, shape, dev)
+        for t, name, shape in ((q, "q", keys), (k, "k", keys), (v, "v", (Bsz, L, H, P))):
+            _check_rows(t, name, dtype, shape, dev)
+    if Bsz > 0 and L > 1:
+        (qb, qs, qh, q1), (kb, ks, kh, k1), (vb, vs, vh, v1) = q.stride(), k.stride(), v.stride()
+        plain = (q1 == 1 and k1 == 1 and v1 == 1 and qh == N and kh == N and vh == P
+                 and qb == L * qs and kb == L * ks and vb == L * vs)
+    else:
+        plain = False
+    if not plain:
+        qs, ks, vs = (_check_rows(t, name, dtype, shape, v.device)
+                      for t, name, shape in ((q, "q", keys), (k, "k", keys), (v, "v", (Bsz, L, H, P))))
+    if T.current_device() != idx:
+        with T.device(idx):
+            return gdr_fwd(q, k, v, dt, beta, dt_bias, A, h0, scale=scale, norm_eps=norm_eps, y=y, h_last=h_last,
+                           workspace=workspace, stream=stream)
     made = []
-    qs = _row_stride(q, "q", dtype, (Bsz, L, G, N), dev, idx)
-    ks = _row_stride(k, "k", dtype, (Bsz, L, G, N), dev, idx)
-    vs = _row_stride(v, "v", dtype, (Bsz, L, H, P), dev, idx)
-    _fits(dt, "dt", dtype, (Bsz, L, H), dev, idx)
-    _fits(beta, "beta", dtype, (Bsz, L, H), dev, idx)
-    _fits(A, "A", f32, (H,), dev, idx)
-    if dt_bias is not None:
-        _fits(dt_bias, "dt_bias", f32, (H,), dev, idx)
-    state = (Bsz, H, P, N)
-    if h0 is not None:
-        _fits(h0, "h0", f32, state, dev, idx)
     if y is None:
-        y = T.empty((Bsz, L, H, P), dtype=dtype, device=dev)
+        y = v.new_empty((Bsz, L, H, P))
         made.append(y)
-    else:
-        _fits(y, "y", dtype, (Bsz, L, H, P), dev, idx)
     if h_last is None:
-        h_last = T.empty(state, dtype=f32, device=dev)
+        h_last = A.new_empty(state)
         made.append(h_last)
-    else:
-        _fits(h_last, "h_last", f32, state, dev, idx)
-    ws_bytes = T.lib.mamba_gdr_workspace_size(Bsz, L, H, P, N, G, act)
-    have = 0 if workspace is None else workspace.nbytes
-    if workspace is None or have < ws_bytes:
-        have = max(ws_bytes, 256)
-        workspace = T.empty(have, dtype=T.u8, device=dev)
-        made.append(workspace)
-    st = _call_on(T, dev, idx, T.lib.mamba_gdr_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), beta.data_ptr(),
-                  None if dt_bias is None else dt_bias.data_ptr(), A.data_ptr(), None if h0 is None else h0.data_ptr(),
-                  y.data_ptr(), h_last.data_ptr(), Bsz, L, G, H, P, N, qs, ks, vs, N ** -0.5 if scale is None else scale,
-                  norm_eps, act, workspace.data_ptr(), have, T.raw_stream(idx) if stream is None else stream.cuda_stream)
-    if st != 0:
-        raise MixerError(st, "mamba_gdr_fwd")
+    while True:
+        if workspace is None:
+            have = max(T.lib.mamba_gdr_workspace_size(Bsz, L, H, P, N, G, act), 256)
+            workspace = v.new_empty(have, dtype=T.u8)
+            made.append(workspace)
+        else:
+            if workspace.get_device() != idx:
+                raise ValueError(f"workspace is on {workspace.device}, expected {v.device}")
+            have = workspace.nbytes
+        st = T.lib.mamba_gdr_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), beta.data_ptr(),
+                                 None if dt_bias is None else dt_bias.data_ptr(), A.data_ptr(),
+                                 None if h0 is None else h0.data_ptr(), y.data_ptr(), h_last.data_ptr(),
+                                 Bsz, L, G, H, P, N, qs, ks, vs, N ** -0.5 if scale is None else scale, norm_eps, act,
+                                 workspace.data_ptr(), have, T.raw_stream(idx) if stream is None else stream.cuda_stream)
+        if st == 0:
+            break
+        if st != _ERR_WORKSPACE or have >= T.lib.mamba_gdr_workspace_size(Bsz, L, H, P, N, G, act):
+            raise MixerError(st, "mamba_gdr_fwd")
+        workspace = None          # the one given is too small
     if stream is not None:
         _keep_alive_on(made, (stream,))
     return y, h_last
@@ -925,33 +932,47 @@ def gdr_state_update(q, k, v, dt, beta, dt_bias, A, state, *, scale=None, norm_e
     spaced), dt and beta [B,H], dt_bias/A [H] fp32 (dt_bias may be None).  scale
     and norm_eps as gdr_fwd.  Returns y [B,H,P], allocated if not given."""
     T = _torch_names or _names()
-    f32, dtype = T.f32, v.dtype
+    f32, dtype, idx = T.f32, v.dtype, v.get_device()
     act = T.codes.get(dtype)
     if act is None:
         _act_code(dtype)
     Bsz, H, P = v.shape
     G, N = q.shape[1:]
-    dev, idx = v.device, v.get_device()
-    qs = _row_stride(q, "q", dtype, (Bsz, G, N), dev, idx)
-    ks = _row_stride(k, "k", dtype, (Bsz, G, N), dev, idx)
-    vs = _row_stride(v, "v", dtype, (Bsz, H, P), dev, idx)
-    _fits(dt, "dt", dtype, (Bsz, H), dev, idx)
-    _fits(beta, "beta", dtype, (Bsz, H), dev, idx)
-    _fits(A, "A", f32, (H,), dev, idx)
-    if dt_bias is not None:
-        _fits(dt_bias, "dt_bias", f32, (H,), dev, idx)
-    if state is None:
-        raise ValueError("state must be given")
-    _fits(state, "state", f32, (Bsz, H, P, N), dev, idx)
+    tokens, keys = (Bsz, H), (Bsz, G, N)
+    if not (idx >= 0 and q.dtype is dtype and k.dtype is dtype and q.get_device() == idx and k.get_device() == idx
+            and k.shape == keys and A is not None and state is not None
+            and dt.shape == tokens and dt.dtype is dtype and dt.get_device() == idx and dt.is_contiguous()
+            and beta.shape == tokens and beta.dtype is dtype and beta.get_device() == idx and beta.is_contiguous()
+            and A.shape == (H,) and A.dtype is f32 and A.get_device() == idx and A.is_contiguous()
+            and (dt_bias is None or (dt_bias.shape == (H,) and dt_bias.dtype is f32 and dt_bias.get_device() == idx
+                                     and dt_bias.is_contiguous()))
+            and state.shape == (Bsz, H, P, N) and state.dtype is f32 and state.get_device() == idx and state.is_contiguous()
+            and (y is None or (y.shape == v.shape and y.dtype is dtype and y.get_device() == idx and y.is_contiguous()))):
+        dev = v.device
+        for t, name, want, shape in ((dt, "dt", dtype, tokens), (beta, "beta", dtype, tokens), (A, "A", f32, (H,)),
+                                     (state, "state", f32, (Bsz, H, P, N))):
+            _required(t, name)
+            _check(t, name, want, shape, dev)
+        _check(dt_bias, "dt_bias", f32, (H,), dev)
+        _check(y, "y", dtype, (Bsz, H, P), dev)
+        for t, name, shape in ((q, "q", keys), (k, "k", keys), (v, "v", (Bsz, H, P))):
+            _check_rows(t, name, dtype, shape, dev)
+    (qs, qh, q1), (ks, kh, k1), (vs, vh, v1) = q.stride(), k.stride(), v.stride()
+    if Bsz == 1:                  # one row of each: as far apart as dense ones
+        qs, ks, vs = G * N, G * N, H * P
+    if not (Bsz > 0 and q1 == 1 and k1 == 1 and v1 == 1 and qh == N and kh == N and vh == P):
+        qs, ks, vs = (_check_rows(t, name, dtype, shape, v.device)
+                      for t, name, shape in ((q, "q", keys), (k, "k", keys), (v, "v", (Bsz, H, P))))
+    if T.current_device() != idx:
+        with T.device(idx):
+            return gdr_state_update(q, k, v, dt, beta, dt_bias, A, state, scale=scale, norm_eps=norm_eps, y=y, stream=stream)
     own = y is None
     if own:
-        y = T.empty((Bsz, H, P), dtype=dtype, device=dev)
-    else:
-        _fits(y, "y", dtype, (Bsz, H, P), dev, idx)
-    st = _call_on(T, dev, idx, T.lib.mamba_gdr_state_update, q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(),
-                  beta.data_ptr(), None if dt_bias is None else dt_bias.data_ptr(), A.data_ptr(), state.data_ptr(),
-                  y.data_ptr(), Bsz, G, H, P, N, qs, ks, vs, N ** -0.5 if scale is None else scale, norm_eps, act,
-                  T.raw_stream(idx) if stream is None else stream.cuda_stream)
+        y = v.new_empty((Bsz, H, P))
+    st = T.lib.mamba_gdr_state_update(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), beta.data_ptr(),
+                                      None if dt_bias is None else dt_bias.data_ptr(), A.data_ptr(), state.data_ptr(),
+                                      y.data_ptr(), Bsz, G, H, P, N, qs, ks, vs, N ** -0.5 if scale is None else scale,
+                                      norm_eps, act, T.raw_stream(idx) if stream is None else stream.cuda_stream)
     if st != 0:
         raise MixerError(st, "mamba_gdr_state_update")
     if own and stream is not None:
@@ -965,28 +986,34 @@ def proj_q4(x, W, scales, zeros=None, *, group=128, out=None, out_dtype=None, st
     and zeros [N,K/group] bf16 (zeros None: 8), weight = scale (number - zero).
     out [M,N] fp32 (default) or bf16, allocated if not given."""
     T = _torch_names or _names()
-    bf = T.bf16
+    bf, idx = T.bf16, x.get_device()
     M, K = x.shape
     N = W.shape[0]
-    dev, idx = x.device, x.get_device()
     if group <= 0:
         raise ValueError(f"group must be positive, got {group}")
-    _fits(x, "x", bf, (M, K), dev, idx)
-    _fits(W, "W", T.u8, (N, K // 2), dev, idx)
-    _fits(scales, "scales", bf, (N, K // group), dev, idx)
-    if zeros is not None:
-        _fits(zeros, "zeros", bf, (N, K // group), dev, idx)
     dtype = out_dtype or (out.dtype if out is not None else T.f32)
     code = T.codes.get(dtype)
     if code is None:
         _act_code(dtype)
+    groups = (N, K // group)
+    if not (idx >= 0 and x.dtype is bf and x.is_contiguous()
+            and W.shape == (N, K // 2) and W.dtype is T.u8 and W.get_device() == idx and W.is_contiguous()
+            and scales.shape == groups and scales.dtype is bf and scales.get_device() == idx and scales.is_contiguous()
+            and (zeros is None or (zeros.shape == groups and zeros.dtype is bf and zeros.get_device() == idx
+                                   and zeros.is_contiguous()))
+            and (out is None or (out.shape == (M, N) and out.dtype is dtype and out.get_device() == idx
+                                 and out.is_contiguous()))):
+        for t, name, want, shape in ((x, "x", bf, (M, K)), (W, "W", T.u8, (N, K // 2)), (scales, "scales", bf, groups),
+                                     (zeros, "zeros", bf, groups), (out, "out", dtype, (M, N))):
+            _check(t, name, want, shape, x.device)
+    if T.current_device() != idx:
+        with T.device(idx):
+            return proj_q4(x, W, scales, zeros, group=group, out=out, out_dtype=out_dtype, stream=stream)
     own = out is None
     if own:
-        out = T.empty((M, N), dtype=dtype, device=dev)
-    else:
-        _fits(out, "out", dtype, (M, N), dev, idx)
-    st = _call_on(T, dev, idx, T.lib.mamba_proj_q4, x.data_ptr(), W.data_ptr(), scales.data_ptr(),
-                  None if zeros is None else zeros.data_ptr(), out.data_ptr(), M, N, K, group, code, T.raw_stream(idx) if stream is None else stream.cuda_stream)
+        out = x.new_empty((M, N), dtype=dtype)
+    st = T.lib.mamba_proj_q4(x.data_ptr(), W.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+                             out.data_ptr(), M, N, K, group, code, T.raw_stream(idx) if stream is None else stream.cuda_stream)
     if st != 0:
         raise MixerError(st, "mamba_proj_q4")
     if own and stream is not None:

@@ -9,8 +9,8 @@
 // with q_t and k_t divided by sqrt(sum of squares + eps) when the call
 // normalises them.
 //
-// gdr_recurrent_kernel runs that as it stands, token by token: the one-token
-// step (decode), short calls and fp32 activations.  gdr_prep_kernel and
+// gdr_recurrent_kernel runs that as it stands for one token (decode),
+// gdr_tokens_kernel token by token: short calls and fp32 activations.  gdr_prep_kernel and
 // gdr_scan_kernel run longer bf16 calls in chunks of 64 tokens on the tensor
 // cores.
 #pragma once
@@ -18,6 +18,7 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 
+#include "m3.cuh"
 #include "mixer_common.cuh"
 #include "proj_gemm.cuh"
 #include "ssd.cuh"
@@ -178,6 +179,195 @@ gdr_recurrent_kernel(const GdrParams p)
         }
         if (e < RPT) yp[4 * e] = Act<T>::from_f32(yv);
         yp += static_cast<int64_t>(p.H) * p.P;
+    }
+#pragma unroll
+    for (int r = 0; r < RPT; ++r)
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            *reinterpret_cast<float4*>(p.h_last + (srow + 4 * r) * N + 4 * e + 32 * m) = s[r][m];
+}
+
+// The same for calls of several tokens.  A token's path is what bounds those
+// (two sums over the state, one update), so nothing else is on it: blocks of 8
+// tokens of k, q and v come through a ring of asynchronous copies two blocks
+// ahead, and each token's decay, strength, norms and k . q are worked out once
+// per CTA, a block ahead.  2 x 200 fp32 tokens of 16 heads (128 x 64): 90 us
+// with the next token's loads in registers (a load's latency a token).
+constexpr int kGdrBlock = 8;          // tokens
+template <typename T, int N, int RPT>
+struct GdrTokensLayout {
+    static constexpr int rows = kGdrRecThreads / 8 * RPT;
+    static constexpr int k_off = 0, q_off = k_off + kGdrBlock * N * sizeof(T), v_off = q_off + kGdrBlock * N * sizeof(T);
+    static constexpr int stage_bytes = v_off + kGdrBlock * rows * sizeof(T);
+    static constexpr int stages = 3;
+};
+
+template <typename T, int N, int RPT>
+__global__ void __launch_bounds__(kGdrRecThreads)
+gdr_tokens_kernel(const GdrParams p)
+{
+    using Lay = GdrTokensLayout<T, N, RPT>;
+    constexpr int M = N / 32;
+    constexpr int kRows = Lay::rows;
+    __shared__ __align__(16) unsigned char ring[Lay::stages * Lay::stage_bytes];
+    __shared__ float4 tok[2][kGdrBlock][2];      // {a, b, 1/|k|, scale/|q|}, {k . q with both factors, ..}
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int e = lane & 7, sub = lane >> 3;
+    const int tiles = p.P / kRows;
+    const int h = blockIdx.x / tiles, b = blockIdx.y;
+    const int g = h / (p.H / p.G);
+    const int first = (blockIdx.x - h * tiles) * kRows, mine = warp * 4 * RPT + sub;   // row r of this lane: first + mine + 4 r
+    if (p.status && tid == 0 && blockIdx.x == 0 && blockIdx.y == 0) p.status[1] = p.status_epoch;
+
+    const int64_t t_first = static_cast<int64_t>(b) * p.L;
+    const T* kp = static_cast<const T*>(p.k) + t_first * p.k_stride + g * N;
+    const T* qp = static_cast<const T*>(p.q) + t_first * p.q_stride + g * N;
+    const T* vp = static_cast<const T*>(p.v) + t_first * p.v_stride + static_cast<int64_t>(h) * p.P + first;
+    const T* dtp = static_cast<const T*>(p.dt) + t_first * p.H + h;
+    const T* bp = static_cast<const T*>(p.beta) + t_first * p.H + h;
+    const int64_t blocks = (p.L + kGdrBlock - 1) / kGdrBlock;
+
+    auto request = [&](int64_t blk) {
+        if (blk < blocks) {
+            unsigned char* st = ring + static_cast<int>(blk % Lay::stages) * Lay::stage_bytes;
+            constexpr int el = 16 / sizeof(T), nk = N / el, nv = kRows / el, per = 2 * nk + nv;
+            for (int i = tid; i < kGdrBlock * per; i += kGdrRecThreads) {
+                const int t = i / per, c = i - t * per;
+                const int64_t at = blk * kGdrBlock + t;
+                if (at >= p.L) break;
+                if (c < nk) cp_async16(st + Lay::k_off + (t * N + c * el) * sizeof(T), kp + at * p.k_stride + c * el);
+                else if (c < 2 * nk) cp_async16(st + Lay::q_off + (t * N + (c - nk) * el) * sizeof(T), qp + at * p.q_stride + (c - nk) * el);
+                else cp_async16(st + Lay::v_off + (t * kRows + (c - 2 * nk) * el) * sizeof(T), vp + at * p.v_stride + (c - 2 * nk) * el);
+            }
+        }
+        cp_async_commit();
+    };
+    // lane 0 of warp w: dt and beta of a block's tokens w and w + 4
+    float dtn[2], bn[2];
+    const float bias = p.dt_bias ? p.dt_bias[h] : 0.0f, A = p.A[h];
+    auto fetch_gates = [&](int64_t blk) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int64_t at = blk * kGdrBlock + warp + 4 * k;
+            if (lane == 0 && at < p.L) {
+                dtn[k] = Act<T>::load(dtp + at * p.H);
+                bn[k] = Act<T>::load(bp + at * p.H);
+            }
+        }
+    };
+    auto work_out = [&](int64_t blk) {
+        const unsigned char* st = ring + static_cast<int>(blk % Lay::stages) * Lay::stage_bytes;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int t = warp + 4 * k;
+            float kk = 0.0f, qq = 0.0f, kq = 0.0f;
+            if (blk * kGdrBlock + t < p.L) {       // the same for the warp
+                const T* kr = reinterpret_cast<const T*>(st + Lay::k_off) + t * N;
+                const T* qr = reinterpret_cast<const T*>(st + Lay::q_off) + t * N;
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const float kv = Act<T>::load(kr + lane + 32 * m), qv = Act<T>::load(qr + lane + 32 * m);
+                    kk = fmaf(kv, kv, kk);
+                    qq = fmaf(qv, qv, qq);
+                    kq = fmaf(kv, qv, kq);
+                }
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    kk += __shfl_xor_sync(kFull, kk, o);
+                    qq += __shfl_xor_sync(kFull, qq, o);
+                    kq += __shfl_xor_sync(kFull, kq, o);
+                }
+                if (lane == 0) {
+                    const float rk = p.eps > 0.0f ? rsqrtf(kk + p.eps) : 1.0f;
+                    const float rq = (p.eps > 0.0f ? rsqrtf(qq + p.eps) : 1.0f) * p.scale;
+                    tok[blk & 1][t][0] = make_float4(expf(MathExact::step(dtn[k], bias) * A), 1.0f / (1.0f + expf(-bn[k])), rk, rq);
+                    tok[blk & 1][t][1].x = kq * rk * rq;
+                }
+            }
+        }
+    };
+    request(0);
+    request(1);
+    fetch_gates(0);
+
+    const int64_t srow = (static_cast<int64_t>(b) * p.H + h) * p.P + first + mine;
+    float4 s[RPT][M];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r)
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            s[r][m] = p.h0 ? *reinterpret_cast<const float4*>(p.h0 + (srow + 4 * r) * N + 4 * e + 32 * m)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+    T* yp = static_cast<T*>(p.y) + (t_first * p.H + h) * p.P + first + mine;
+
+    cp_async_wait<0>();
+    __syncthreads();
+    work_out(0);
+    fetch_gates(1);
+    for (int64_t blk = 0; blk < blocks; ++blk) {
+        // the next block is there, this one's tokens are worked out, and the
+        // block before is done with
+        cp_async_wait<0>();
+        __syncthreads();
+        request(blk + 2);
+        work_out(blk + 1);
+        fetch_gates(blk + 2);
+        const unsigned char* st = ring + static_cast<int>(blk % Lay::stages) * Lay::stage_bytes;
+        const int n_tok = static_cast<int>(min(static_cast<int64_t>(kGdrBlock), p.L - blk * kGdrBlock));
+#pragma unroll 2
+        for (int t = 0; t < n_tok; ++t) {
+            const T* kr = reinterpret_cast<const T*>(st + Lay::k_off) + t * N + 4 * e;
+            const T* qr = reinterpret_cast<const T*>(st + Lay::q_off) + t * N + 4 * e;
+            const T* vr = reinterpret_cast<const T*>(st + Lay::v_off) + t * kRows + mine;
+            float4 k[M], q[M];
+            float v[RPT];
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                k[m] = load4(kr + 32 * m);
+                q[m] = load4(qr + 32 * m);
+            }
+#pragma unroll
+            for (int r = 0; r < RPT; ++r) v[r] = Act<T>::load(vr + 4 * r);
+            const float4 f = tok[blk & 1][t][0];
+            const float rkq = tok[blk & 1][t][1].x;
+            float ks[RPT], qs[RPT];
+#pragma unroll
+            for (int r = 0; r < RPT; ++r) {
+                float ka[M], qa[M];
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    ka[m] = dot4(s[r][m], k[m], 0.0f);
+                    qa[m] = dot4(s[r][m], q[m], 0.0f);
+                }
+                ks[r] = M == 4 ? (ka[0] + ka[1]) + (ka[2] + ka[M - 1]) : ka[0] + ka[1];
+                qs[r] = M == 4 ? (qa[0] + qa[1]) + (qa[2] + qa[M - 1]) : qa[0] + qa[1];
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+#pragma unroll
+                for (int r = 0; r < RPT; ++r) {
+                    ks[r] += __shfl_xor_sync(kFull, ks[r], o);
+                    qs[r] += __shfl_xor_sync(kFull, qs[r], o);
+                }
+            }
+            float yv = 0.0f;      // lane e < RPT: row e's output
+#pragma unroll
+            for (int r = 0; r < RPT; ++r) {
+                const float u = f.y * (v[r] - f.x * (ks[r] * f.z));
+                const float out = fmaf(f.x * f.w, qs[r], u * rkq);
+                if (e == r) yv = out;
+                const float uk = u * f.z;
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    s[r][m].x = fmaf(f.x, s[r][m].x, uk * k[m].x);
+                    s[r][m].y = fmaf(f.x, s[r][m].y, uk * k[m].y);
+                    s[r][m].z = fmaf(f.x, s[r][m].z, uk * k[m].z);
+                    s[r][m].w = fmaf(f.x, s[r][m].w, uk * k[m].w);
+                }
+            }
+            if (e < RPT) yp[4 * e] = Act<T>::from_f32(yv);
+            yp += static_cast<int64_t>(p.H) * p.P;
+        }
     }
 #pragma unroll
     for (int r = 0; r < RPT; ++r)
@@ -747,6 +937,10 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         mbar_init(&in_full[2], kGdrWarps);
         fence_mbar_init();
     }
+    // What the kernels before wrote is read from here on.  All of tensor memory
+    // is allocated after that, too: a block of theirs that has yet to allocate
+    // could otherwise wait for this one, and this one for it.
+    grid_dependency_wait();
     if (warp == kGdrWarps) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
@@ -1039,8 +1233,9 @@ gdr_segment_kernel(const GdrChunkParams p)
         mbar_init(&full[0], 1);
         mbar_init(&full[1], 1);
         fence_mbar_init();
-        if (p.segs > 2) request(1);
     }
+    grid_dependency_wait();
+    if (n == 0 && p.segs > 2) request(1);
     __syncthreads();
     float s[kGdrSegRows];
     for (int seg = 0; seg + 1 < p.segs; ++seg) {

@@ -1939,7 +1939,9 @@ mm::GdrParams gdr_params(const GdrArgs& a) {
 template <typename T, int N, int RPT>
 cudaError_t launch_gdr_recurrent_t(const mm::GdrParams& p, int64_t batch, cudaStream_t s) {
     const dim3 grid(static_cast<unsigned>(p.H * (p.P / (mm::kGdrRecThreads / 8 * RPT))), static_cast<unsigned>(batch));
-    mm::gdr_recurrent_kernel<T, N, RPT><<<grid, mm::kGdrRecThreads, forced_launch_failure() ? (1 << 20) : 0, s>>>(p);
+    const int smem = forced_launch_failure() ? (1 << 20) : 0;
+    if (p.L > 1) mm::gdr_tokens_kernel<T, N, RPT><<<grid, mm::kGdrRecThreads, smem, s>>>(p);
+    else mm::gdr_recurrent_kernel<T, N, RPT><<<grid, mm::kGdrRecThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
 // State rows per lane: four once the grid fills the SMs with them (fewer
@@ -2026,6 +2028,23 @@ bool encode_gdr_rows(CUtensorMap* m, const void* base, int64_t cols, int64_t str
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch that may start while the kernel before it in the stream still runs
+// (it waits for that kernel's writes itself).
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
 template <int N>
 mm_status launch_gdr_chunked(const GdrArgs& a, const GdrPlan& pl, unsigned char* w, unsigned long long epoch, cudaStream_t s) {
     CUtensorMap tq, tk, tv, tt;
@@ -2074,15 +2093,20 @@ mm_status launch_gdr_chunked(const GdrArgs& a, const GdrPlan& pl, unsigned char*
         const unsigned tiles = static_cast<unsigned>(p.P / mm::kGdrTile), smem = fail ? (1 << 20) : mm::GdrScanLayout<N>::smem_bytes;
         const unsigned heads = static_cast<unsigned>(p.H), batch = static_cast<unsigned>(a.batch);
         if (p.segs > 1) {
-            mm::gdr_scan_kernel<N, true><<<dim3(tiles + N / mm::kGdrTile, heads, batch * (p.segs - 1)), mm::kGdrScanThreads, smem,
-                                           s>>>(p, tq, tk, tv, tt);
-            if (cudaGetLastError() != cudaSuccess) return MM_ERR_CUDA;
-            mm::gdr_segment_kernel<N><<<dim3(static_cast<unsigned>(p.P / mm::kGdrSegRows), heads, batch), N,
-                                        mm::GdrSegmentLayout<N>::smem_bytes, s>>>(p);
-            if (cudaGetLastError() != cudaSuccess) return MM_ERR_CUDA;
+            const unsigned seg_smem = fail ? (1 << 20) : mm::GdrSegmentLayout<N>::smem_bytes;
+            if (launch_dependent(mm::gdr_scan_kernel<N, true>, dim3(tiles + N / mm::kGdrTile, heads, batch * (p.segs - 1)),
+                                 mm::kGdrScanThreads, smem, s, p, tq, tk, tv, tt) != cudaSuccess ||
+                launch_dependent(mm::gdr_segment_kernel<N>, dim3(static_cast<unsigned>(p.P / mm::kGdrSegRows), heads, batch), N,
+                                 seg_smem, s, p) != cudaSuccess) {
+                cudaGetLastError();
+                return MM_ERR_CUDA;
+            }
         }
-        mm::gdr_scan_kernel<N, false><<<dim3(tiles, heads, batch * p.segs), mm::kGdrScanThreads, smem, s>>>(p, tq, tk, tv, tt);
-        if (cudaGetLastError() != cudaSuccess) return MM_ERR_CUDA;
+        if (launch_dependent(mm::gdr_scan_kernel<N, false>, dim3(tiles, heads, batch * p.segs), mm::kGdrScanThreads, smem, s, p, tq,
+                             tk, tv, tt) != cudaSuccess) {
+            cudaGetLastError();
+            return MM_ERR_CUDA;
+        }
     }
     return MM_OK;
 }
