@@ -187,13 +187,25 @@ gdr_recurrent_kernel(const GdrParams p)
             *reinterpret_cast<float4*>(p.h_last + (srow + 4 * r) * N + 4 * e + 32 * m) = s[r][m];
 }
 
-// The same for calls of several tokens.  A token's path is what bounds those
-// (two sums over the state, one update), so nothing else is on it: blocks of 8
-// tokens of k, q and v come through a ring of asynchronous copies two blocks
-// ahead, and each token's decay, strength, norms and k . q are worked out once
-// per CTA, a block ahead.  2 x 200 fp32 tokens of 16 heads (128 x 64): 90 us
-// with the next token's loads in registers (a load's latency a token).
-constexpr int kGdrBlock = 8;          // tokens
+// The same for calls of several tokens.  What bounds those is the path from
+// one token's sums over the state to the next one's, so four tokens share it:
+// with c_i the product of the group's decays up to token i and D_ij that of
+// those after j,
+//
+//     u_i = b_i (v_i - c_i S k_i - sum_{j<i} D_ij (k_i . k_j) u_j)
+//     y_i = scale (c_i S q_i + sum_{j<=i} D_ij (q_i . k_j) u_j)
+//     S  <- c_3 S + sum_j D_3j u_j k_j^T
+//
+// needs S once for all eight sums and once for the update.  The coefficients
+// are the same for every row: two helper warps, one for each group of a block
+// of 8 tokens, work them out a block ahead and keep the copies of k, q and v
+// (a ring of asynchronous copies) two blocks ahead, beside the four warps that
+// hold the state.  All in fp32.  2 x 200 fp32 tokens of 16 heads (128 x 64):
+// 90 us with the next token's loads in registers; 68 with a ring that all
+// warps fill, a token at a time (1900 cycles a block went into its addresses).
+constexpr int kGdrBlock = 8;          // tokens of a ring slot: two groups
+constexpr int kGdrGroup = 4;
+constexpr int kGdrTokThreads = kGdrRecThreads + 64;
 template <typename T, int N, int RPT>
 struct GdrTokensLayout {
     static constexpr int rows = kGdrRecThreads / 8 * RPT;
@@ -201,95 +213,149 @@ struct GdrTokensLayout {
     static constexpr int stage_bytes = v_off + kGdrBlock * rows * sizeof(T);
     static constexpr int stages = 3;
 };
+// Of a group of four tokens, with the norms and the scale in them.
+struct GdrGroup {
+    float alpha[4];     // c_i, of S k_i
+    float beta[4];      // scale c_i, of S q_i
+    float b[4];         // b_i
+    float w[4];         // D_3j, of u_j k_j
+    float kk[4][4];     // D_ij (k_i . k_j), j < i; [0][0] is c_3
+    float qk[4][4];     // scale D_ij (q_i . k_j), j <= i
+};
 
 template <typename T, int N, int RPT>
-__global__ void __launch_bounds__(kGdrRecThreads)
+__global__ void __launch_bounds__(kGdrTokThreads)
 gdr_tokens_kernel(const GdrParams p)
 {
     using Lay = GdrTokensLayout<T, N, RPT>;
     constexpr int M = N / 32;
     constexpr int kRows = Lay::rows;
     __shared__ __align__(16) unsigned char ring[Lay::stages * Lay::stage_bytes];
-    __shared__ float4 tok[2][kGdrBlock][2];      // {a, b, 1/|k|, scale/|q|}, {k . q with both factors, ..}
+    __shared__ __align__(16) GdrGroup coef[2][2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int e = lane & 7, sub = lane >> 3;
     const int tiles = p.P / kRows;
     const int h = blockIdx.x / tiles, b = blockIdx.y;
     const int g = h / (p.H / p.G);
-    const int first = (blockIdx.x - h * tiles) * kRows, mine = warp * 4 * RPT + sub;   // row r of this lane: first + mine + 4 r
+    const int first = (blockIdx.x - h * tiles) * kRows;
     if (p.status && tid == 0 && blockIdx.x == 0 && blockIdx.y == 0) p.status[1] = p.status_epoch;
 
     const int64_t t_first = static_cast<int64_t>(b) * p.L;
-    const T* kp = static_cast<const T*>(p.k) + t_first * p.k_stride + g * N;
-    const T* qp = static_cast<const T*>(p.q) + t_first * p.q_stride + g * N;
-    const T* vp = static_cast<const T*>(p.v) + t_first * p.v_stride + static_cast<int64_t>(h) * p.P + first;
-    const T* dtp = static_cast<const T*>(p.dt) + t_first * p.H + h;
-    const T* bp = static_cast<const T*>(p.beta) + t_first * p.H + h;
-    const int64_t blocks = (p.L + kGdrBlock - 1) / kGdrBlock;
+    const int L = static_cast<int>(p.L), blocks = (L + kGdrBlock - 1) / kGdrBlock;
+    auto slot = [&](int blk) { return ring + blk % Lay::stages * Lay::stage_bytes; };
 
-    auto request = [&](int64_t blk) {
-        if (blk < blocks) {
-            unsigned char* st = ring + static_cast<int>(blk % Lay::stages) * Lay::stage_bytes;
-            constexpr int el = 16 / sizeof(T), nk = N / el, nv = kRows / el, per = 2 * nk + nv;
-            for (int i = tid; i < kGdrBlock * per; i += kGdrRecThreads) {
-                const int t = i / per, c = i - t * per;
-                const int64_t at = blk * kGdrBlock + t;
-                if (at >= p.L) break;
-                if (c < nk) cp_async16(st + Lay::k_off + (t * N + c * el) * sizeof(T), kp + at * p.k_stride + c * el);
-                else if (c < 2 * nk) cp_async16(st + Lay::q_off + (t * N + (c - nk) * el) * sizeof(T), qp + at * p.q_stride + (c - nk) * el);
-                else cp_async16(st + Lay::v_off + (t * kRows + (c - 2 * nk) * el) * sizeof(T), vp + at * p.v_stride + (c - 2 * nk) * el);
-            }
-        }
-        cp_async_commit();
-    };
-    // lane 0 of warp w: dt and beta of a block's tokens w and w + 4
-    float dtn[2], bn[2];
-    const float bias = p.dt_bias ? p.dt_bias[h] : 0.0f, A = p.A[h];
-    auto fetch_gates = [&](int64_t blk) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int64_t at = blk * kGdrBlock + warp + 4 * k;
-            if (lane == 0 && at < p.L) {
-                dtn[k] = Act<T>::load(dtp + at * p.H);
-                bn[k] = Act<T>::load(bp + at * p.H);
-            }
-        }
-    };
-    auto work_out = [&](int64_t blk) {
-        const unsigned char* st = ring + static_cast<int>(blk % Lay::stages) * Lay::stage_bytes;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int t = warp + 4 * k;
-            float kk = 0.0f, qq = 0.0f, kq = 0.0f;
-            if (blk * kGdrBlock + t < p.L) {       // the same for the warp
-                const T* kr = reinterpret_cast<const T*>(st + Lay::k_off) + t * N;
-                const T* qr = reinterpret_cast<const T*>(st + Lay::q_off) + t * N;
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    const float kv = Act<T>::load(kr + lane + 32 * m), qv = Act<T>::load(qr + lane + 32 * m);
-                    kk = fmaf(kv, kv, kk);
-                    qq = fmaf(qv, qv, qq);
-                    kq = fmaf(kv, qv, kq);
-                }
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    kk += __shfl_xor_sync(kFull, kk, o);
-                    qq += __shfl_xor_sync(kFull, qq, o);
-                    kq += __shfl_xor_sync(kFull, kq, o);
-                }
-                if (lane == 0) {
-                    const float rk = p.eps > 0.0f ? rsqrtf(kk + p.eps) : 1.0f;
-                    const float rq = (p.eps > 0.0f ? rsqrtf(qq + p.eps) : 1.0f) * p.scale;
-                    tok[blk & 1][t][0] = make_float4(expf(MathExact::step(dtn[k], bias) * A), 1.0f / (1.0f + expf(-bn[k])), rk, rq);
-                    tok[blk & 1][t][1].x = kq * rk * rq;
+    if (warp >= kGdrRecThreads / 32) {
+        const T* kp = static_cast<const T*>(p.k) + t_first * p.k_stride + g * N;
+        const T* qp = static_cast<const T*>(p.q) + t_first * p.q_stride + g * N;
+        const T* vp = static_cast<const T*>(p.v) + t_first * p.v_stride + static_cast<int64_t>(h) * p.P + first;
+        const int half = warp - kGdrRecThreads / 32;
+        // this warp's group of a block: four tokens of k, q and v in 16-byte pieces
+        auto request = [&](int blk) {
+            if (blk < blocks) {
+                unsigned char* st = slot(blk);
+                constexpr int el = 16 / sizeof(T), nk = N / el, nv = kRows / el, per = 2 * nk + nv;
+#pragma unroll 2
+                for (int i = lane; i < kGdrGroup * per; i += 32) {
+                    const int t = half * kGdrGroup + i / per, c = i % per;
+                    const int64_t at = blk * kGdrBlock + t;
+                    const bool in_k = c < nk, in_q = c < 2 * nk;
+                    const int col = (in_k ? c : in_q ? c - nk : c - 2 * nk) * el;
+                    unsigned char* dst = st + (in_k ? Lay::k_off : in_q ? Lay::q_off : Lay::v_off) +
+                                         (t * (in_q ? N : kRows) + col) * sizeof(T);
+                    if (at < L) cp_async16(dst, (in_k ? kp : in_q ? qp : vp) + at * (in_k ? p.k_stride : in_q ? p.q_stride : p.v_stride) + col);
+                    else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);       // past the sequence
                 }
             }
+            cp_async_commit();
+        };
+        // lanes 0..3: dt and beta of the group's tokens
+        const T* dtp = static_cast<const T*>(p.dt) + (t_first + half * kGdrGroup + lane) * p.H + h;
+        const T* bp = static_cast<const T*>(p.beta) + (t_first + half * kGdrGroup + lane) * p.H + h;
+        float dtn = 0.0f, bn = 0.0f;
+        const float bias = p.dt_bias ? p.dt_bias[h] : 0.0f, A = p.A[h];
+        auto fetch_gates = [&](int blk) {
+            if (lane < kGdrGroup && blk * kGdrBlock + half * kGdrGroup + lane < L) {
+                dtn = Act<T>::load(dtp + static_cast<int64_t>(blk) * kGdrBlock * p.H);
+                bn = Act<T>::load(bp + static_cast<int64_t>(blk) * kGdrBlock * p.H);
+            }
+        };
+        auto work_out = [&](int blk) {
+            const unsigned char* st = slot(blk);
+            const T* kb = reinterpret_cast<const T*>(st + Lay::k_off) + half * kGdrGroup * N + 4 * e;
+            const T* qb = reinterpret_cast<const T*>(st + Lay::q_off) + half * kGdrGroup * N + 4 * e;
+            float gate = 1.0f, strength = 0.0f;
+            if (lane < kGdrGroup && blk * kGdrBlock + half * kGdrGroup + lane < L) {
+                gate = expf(MathExact::step(dtn, bias) * A);
+                strength = 1.0f / (1.0f + expf(-bn));
+            }
+            // column j = sub: eight lanes for k_i . k_j, q_i . k_j and q_i . q_i, i = 0..3
+            float kk[4] = {}, qk[4] = {}, qq[4] = {};
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const float4 kj = load4(kb + sub * N + 32 * m);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 ki = load4(kb + i * N + 32 * m), qi = load4(qb + i * N + 32 * m);
+                    kk[i] = dot4(ki, kj, kk[i]);
+                    qk[i] = dot4(qi, kj, qk[i]);
+                    qq[i] = dot4(qi, qi, qq[i]);
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    kk[i] += __shfl_xor_sync(kFull, kk[i], o);
+                    qk[i] += __shfl_xor_sync(kFull, qk[i], o);
+                    qq[i] += __shfl_xor_sync(kFull, qq[i], o);
+                }
+            // lane (j = sub, i = e) from here on; lanes e >= 4 repeat them
+            const int i = e & 3, j = sub;
+            const float kij = i == 0 ? kk[0] : i == 1 ? kk[1] : i == 2 ? kk[2] : kk[3];
+            const float qij = i == 0 ? qk[0] : i == 1 ? qk[1] : i == 2 ? qk[2] : qk[3];
+            const float qii = i == 0 ? qq[0] : i == 1 ? qq[1] : i == 2 ? qq[2] : qq[3];
+            const float rq = (p.eps > 0.0f ? rsqrtf(qii + p.eps) : 1.0f) * p.scale;      // of token i
+            const float rd = p.eps > 0.0f ? rsqrtf(kij + p.eps) : 1.0f;                  // the norm on the diagonal
+            const float rki = __shfl_sync(kFull, rd, 9 * i), rkj = __shfl_sync(kFull, rd, 9 * j);
+            float dij = 1.0f, ci = 1.0f, c3 = 1.0f;
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {
+                const float al = __shfl_sync(kFull, gate, l);
+                dij *= l > j && l <= i ? al : 1.0f;
+                ci *= l <= i ? al : 1.0f;
+                c3 *= al;
+            }
+            const float bi = __shfl_sync(kFull, strength, i);
+            GdrGroup& out = coef[blk & 1][half];
+            if (e < 4) {
+                out.kk[i][j] = i == 0 && j == 0 ? c3 : dij * (rki * rkj) * kij;
+                out.qk[i][j] = dij * (rq * rkj) * qij;
+                if (j == 0) {
+                    out.alpha[i] = ci * rki;
+                    out.beta[i] = ci * rq;
+                    out.b[i] = bi;
+                }
+                if (i == 3) out.w[j] = dij * rkj;
+            }
+        };
+        request(0);
+        request(1);
+        fetch_gates(0);
+        cp_async_wait<1>();
+        asm volatile("bar.sync 1, 64;\n" ::: "memory");       // the other helper's copies of the block too
+        work_out(0);
+        fetch_gates(1);
+        for (int blk = 0; blk < blocks; ++blk) {
+            cp_async_wait<0>();
+            __syncthreads();      // block blk + 1 is there, blk's coefficients are, blk - 1 is done with
+            request(blk + 2);
+            if (blk + 1 < blocks) work_out(blk + 1);
+            fetch_gates(blk + 2);
         }
-    };
-    request(0);
-    request(1);
-    fetch_gates(0);
+        return;
+    }
 
+    const int mine = warp * 4 * RPT + sub;   // row r of this lane: first + mine + 4 r
     const int64_t srow = (static_cast<int64_t>(b) * p.H + h) * p.P + first + mine;
     float4 s[RPT][M];
 #pragma unroll
@@ -298,75 +364,91 @@ gdr_tokens_kernel(const GdrParams p)
         for (int m = 0; m < M; ++m)
             s[r][m] = p.h0 ? *reinterpret_cast<const float4*>(p.h0 + (srow + 4 * r) * N + 4 * e + 32 * m)
                            : make_float4(0.f, 0.f, 0.f, 0.f);
-    T* yp = static_cast<T*>(p.y) + (t_first * p.H + h) * p.P + first + mine;
+    // lane e < 4 writes token e of a group
+    const int64_t y_step = static_cast<int64_t>(p.H) * p.P;
+    T* yp = static_cast<T*>(p.y) + (t_first * p.H + h) * p.P + first + mine + e * y_step;
 
-    cp_async_wait<0>();
-    __syncthreads();
-    work_out(0);
-    fetch_gates(1);
-    for (int64_t blk = 0; blk < blocks; ++blk) {
-        // the next block is there, this one's tokens are worked out, and the
-        // block before is done with
-        cp_async_wait<0>();
+    for (int blk = 0; blk < blocks; ++blk) {
         __syncthreads();
-        request(blk + 2);
-        work_out(blk + 1);
-        fetch_gates(blk + 2);
-        const unsigned char* st = ring + static_cast<int>(blk % Lay::stages) * Lay::stage_bytes;
-        const int n_tok = static_cast<int>(min(static_cast<int64_t>(kGdrBlock), p.L - blk * kGdrBlock));
-#pragma unroll 2
-        for (int t = 0; t < n_tok; ++t) {
-            const T* kr = reinterpret_cast<const T*>(st + Lay::k_off) + t * N + 4 * e;
-            const T* qr = reinterpret_cast<const T*>(st + Lay::q_off) + t * N + 4 * e;
-            const T* vr = reinterpret_cast<const T*>(st + Lay::v_off) + t * kRows + mine;
-            float4 k[M], q[M];
-            float v[RPT];
+        const unsigned char* st = slot(blk);
+        const T* kb = reinterpret_cast<const T*>(st + Lay::k_off) + 4 * e;
+        const T* qb = reinterpret_cast<const T*>(st + Lay::q_off) + 4 * e;
+        const T* vb = reinterpret_cast<const T*>(st + Lay::v_off) + mine;
+#pragma unroll 1
+        for (int t = 0; t < kGdrBlock; t += kGdrGroup) {
+            const GdrGroup& c = coef[blk & 1][t / kGdrGroup];
+            float ks[RPT][4], qs[RPT][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int r = 0; r < RPT; ++r) ks[r][j] = qs[r][j] = 0.0f;
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const float4 k = load4(kb + (t + j) * N + 32 * m), q = load4(qb + (t + j) * N + 32 * m);
+#pragma unroll
+                    for (int r = 0; r < RPT; ++r) {
+                        ks[r][j] = dot4(s[r][m], k, ks[r][j]);
+                        qs[r][j] = dot4(s[r][m], q, qs[r][j]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int r = 0; r < RPT; ++r) {
+                        ks[r][j] += __shfl_xor_sync(kFull, ks[r][j], o);
+                        qs[r][j] += __shfl_xor_sync(kFull, qs[r][j], o);
+                    }
+            const float4 al = load4(c.alpha), be = load4(c.beta), bt = load4(c.b), w = load4(c.w);
+            const float4 k1 = load4(c.kk[1]), k2 = load4(c.kk[2]), k3 = load4(c.kk[3]);
+            const float4 q1 = load4(c.qk[1]), q2 = load4(c.qk[2]), q3 = load4(c.qk[3]);
+            const float q00 = c.qk[0][0], c3 = c.kk[0][0];
+            float u[RPT][4], y[RPT];
+#pragma unroll
+            for (int r = 0; r < RPT; ++r) {
+                const T* vr = vb + t * kRows + 4 * r;
+                u[r][0] = bt.x * fmaf(-al.x, ks[r][0], Act<T>::load(vr));
+                u[r][1] = bt.y * fmaf(-k1.x, u[r][0], fmaf(-al.y, ks[r][1], Act<T>::load(vr + kRows)));
+                u[r][2] = bt.z * fmaf(-k2.y, u[r][1], fmaf(-k2.x, u[r][0], fmaf(-al.z, ks[r][2], Act<T>::load(vr + 2 * kRows))));
+                u[r][3] = bt.w * fmaf(-k3.z, u[r][2], fmaf(-k3.y, u[r][1], fmaf(-k3.x, u[r][0],
+                                                                                fmaf(-al.w, ks[r][3], Act<T>::load(vr + 3 * kRows)))));
+                const float y0 = fmaf(q00, u[r][0], be.x * qs[r][0]);
+                const float y1 = fmaf(q1.y, u[r][1], fmaf(q1.x, u[r][0], be.y * qs[r][1]));
+                const float y2 = fmaf(q2.z, u[r][2], fmaf(q2.y, u[r][1], fmaf(q2.x, u[r][0], be.z * qs[r][2])));
+                const float y3 = fmaf(q3.w, u[r][3], fmaf(q3.z, u[r][2], fmaf(q3.y, u[r][1], fmaf(q3.x, u[r][0], be.w * qs[r][3]))));
+                y[r] = e == 0 ? y0 : e == 1 ? y1 : e == 2 ? y2 : y3;
+                u[r][0] *= w.x;
+                u[r][1] *= w.y;
+                u[r][2] *= w.z;
+                u[r][3] *= w.w;
+            }
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-                k[m] = load4(kr + 32 * m);
-                q[m] = load4(qr + 32 * m);
-            }
-#pragma unroll
-            for (int r = 0; r < RPT; ++r) v[r] = Act<T>::load(vr + 4 * r);
-            const float4 f = tok[blk & 1][t][0];
-            const float rkq = tok[blk & 1][t][1].x;
-            float ks[RPT], qs[RPT];
-#pragma unroll
-            for (int r = 0; r < RPT; ++r) {
-                float ka[M], qa[M];
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    ka[m] = dot4(s[r][m], k[m], 0.0f);
-                    qa[m] = dot4(s[r][m], q[m], 0.0f);
-                }
-                ks[r] = M == 4 ? (ka[0] + ka[1]) + (ka[2] + ka[M - 1]) : ka[0] + ka[1];
-                qs[r] = M == 4 ? (qa[0] + qa[1]) + (qa[2] + qa[M - 1]) : qa[0] + qa[1];
-            }
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
 #pragma unroll
                 for (int r = 0; r < RPT; ++r) {
-                    ks[r] += __shfl_xor_sync(kFull, ks[r], o);
-                    qs[r] += __shfl_xor_sync(kFull, qs[r], o);
+                    s[r][m].x *= c3;
+                    s[r][m].y *= c3;
+                    s[r][m].z *= c3;
+                    s[r][m].w *= c3;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 k = load4(kb + (t + j) * N + 32 * m);
+#pragma unroll
+                    for (int r = 0; r < RPT; ++r) {
+                        s[r][m].x = fmaf(u[r][j], k.x, s[r][m].x);
+                        s[r][m].y = fmaf(u[r][j], k.y, s[r][m].y);
+                        s[r][m].z = fmaf(u[r][j], k.z, s[r][m].z);
+                        s[r][m].w = fmaf(u[r][j], k.w, s[r][m].w);
+                    }
                 }
             }
-            float yv = 0.0f;      // lane e < RPT: row e's output
+            const int at = blk * kGdrBlock + t;
+            if (e < 4 && at + e < L)
 #pragma unroll
-            for (int r = 0; r < RPT; ++r) {
-                const float u = f.y * (v[r] - f.x * (ks[r] * f.z));
-                const float out = fmaf(f.x * f.w, qs[r], u * rkq);
-                if (e == r) yv = out;
-                const float uk = u * f.z;
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    s[r][m].x = fmaf(f.x, s[r][m].x, uk * k[m].x);
-                    s[r][m].y = fmaf(f.x, s[r][m].y, uk * k[m].y);
-                    s[r][m].z = fmaf(f.x, s[r][m].z, uk * k[m].z);
-                    s[r][m].w = fmaf(f.x, s[r][m].w, uk * k[m].w);
-                }
-            }
-            if (e < RPT) yp[4 * e] = Act<T>::from_f32(yv);
-            yp += static_cast<int64_t>(p.H) * p.P;
+                for (int r = 0; r < RPT; ++r) yp[at * y_step + 4 * r] = Act<T>::from_f32(y[r]);
         }
     }
 #pragma unroll

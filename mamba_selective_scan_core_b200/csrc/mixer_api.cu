@@ -1936,20 +1936,23 @@ mm::GdrParams gdr_params(const GdrArgs& a) {
     return p;
 }
 
+// kern: RPT state rows a lane of its 128 threads that hold the state
 template <typename T, int N, int RPT>
-cudaError_t launch_gdr_recurrent_t(const mm::GdrParams& p, int64_t batch, cudaStream_t s) {
+cudaError_t launch_gdr_rows(const mm::GdrParams& p, int64_t batch, cudaStream_t s, void (*kern)(mm::GdrParams), int threads) {
     const dim3 grid(static_cast<unsigned>(p.H * (p.P / (mm::kGdrRecThreads / 8 * RPT))), static_cast<unsigned>(batch));
-    const int smem = forced_launch_failure() ? (1 << 20) : 0;
-    if (p.L > 1) mm::gdr_tokens_kernel<T, N, RPT><<<grid, mm::kGdrRecThreads, smem, s>>>(p);
-    else mm::gdr_recurrent_kernel<T, N, RPT><<<grid, mm::kGdrRecThreads, smem, s>>>(p);
+    kern<<<grid, threads, forced_launch_failure() ? (1 << 20) : 0, s>>>(p);
     return cudaGetLastError();
 }
-// State rows per lane: four once the grid fills the SMs with them (fewer
+// State rows per lane: more once the grid fills the SMs with them (fewer
 // reads of q and k per row), one below that (the latency of a row decides).
 template <typename T, int N>
 cudaError_t launch_gdr_recurrent_n(const mm::GdrParams& p, int64_t batch, cudaStream_t s) {
-    const bool wide = batch * p.H * p.P / (mm::kGdrRecThreads / 8 * 4) >= 4 * plan_sms();
-    return wide ? launch_gdr_recurrent_t<T, N, 4>(p, batch, s) : launch_gdr_recurrent_t<T, N, 1>(p, batch, s);
+    const int64_t rows = batch * p.H * p.P / (mm::kGdrRecThreads / 8);        // CTAs of one row a lane
+    if (p.L > 1)
+        return rows >= 16 * plan_sms() ? launch_gdr_rows<T, N, 2>(p, batch, s, mm::gdr_tokens_kernel<T, N, 2>, mm::kGdrTokThreads)
+                                       : launch_gdr_rows<T, N, 1>(p, batch, s, mm::gdr_tokens_kernel<T, N, 1>, mm::kGdrTokThreads);
+    return rows >= 16 * plan_sms() ? launch_gdr_rows<T, N, 4>(p, batch, s, mm::gdr_recurrent_kernel<T, N, 4>, mm::kGdrRecThreads)
+                                   : launch_gdr_rows<T, N, 1>(p, batch, s, mm::gdr_recurrent_kernel<T, N, 1>, mm::kGdrRecThreads);
 }
 mm_status launch_gdr_recurrent(const mm::GdrParams& p, const GdrArgs& a, cudaStream_t s) {
     cudaError_t e;
