@@ -18,7 +18,6 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 
-#include "m3.cuh"
 #include "mixer_common.cuh"
 #include "proj_gemm.cuh"
 #include "ssd.cuh"
@@ -38,6 +37,7 @@ struct GdrParams {
     float* h_last;               // [B][H][P][N]
     int64_t L, q_stride, k_stride, v_stride;
     int H, G, P;
+    unsigned wait_limit;
     float scale, eps;            // eps > 0: q and k are normalised
     unsigned long long* status;  // [0] (epoch << 8) | code of a failure, [1] the call's epoch; or null
     unsigned long long status_epoch;
@@ -51,6 +51,17 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 }
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
     return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+
+// One contiguous bulk copy global -> shared (16-byte aligned, a multiple of 16
+// bytes), completion on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* gsrc, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n"
+                 :: "r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(bytes), "r"(smem_addr(bar)) : "memory");
+}
+// the same answer for every lane of the warp
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned limit) {
+    return __all_sync(kFull, mbar_wait_bounded(bar, parity, limit));
 }
 
 // ---------------------------------------------------------------- token by token
@@ -198,11 +209,11 @@ gdr_recurrent_kernel(const GdrParams p)
 //
 // needs S once for all eight sums and once for the update.  The coefficients
 // are the same for every row: two helper warps, one for each group of a block
-// of 8 tokens, work them out a block ahead and keep the copies of k, q and v
-// (a ring of asynchronous copies) two blocks ahead, beside the four warps that
-// hold the state.  All in fp32.  2 x 200 fp32 tokens of 16 heads (128 x 64):
-// 90 us with the next token's loads in registers; 68 with a ring that all
-// warps fill, a token at a time (1900 cycles a block went into its addresses).
+// of 8 tokens, work them out a block ahead and keep k, q and v (three tensor
+// copies a block; a copy a row takes 90 cycles each to issue) two blocks ahead,
+// beside the four warps that hold the state.  All in fp32.  2 x 200 fp32 tokens
+// of 16 heads (128 x 64): 90 us with the next token's loads in registers, 68
+// a token at a time with a ring that all warps fill, 41 this way.
 constexpr int kGdrBlock = 8;          // tokens of a ring slot: two groups
 constexpr int kGdrGroup = 4;
 constexpr int kGdrTokThreads = kGdrRecThreads + 64;
@@ -212,6 +223,7 @@ struct GdrTokensLayout {
     static constexpr int k_off = 0, q_off = k_off + kGdrBlock * N * sizeof(T), v_off = q_off + kGdrBlock * N * sizeof(T);
     static constexpr int stage_bytes = v_off + kGdrBlock * rows * sizeof(T);
     static constexpr int stages = 3;
+    static_assert(q_off % 128 == 0 && v_off % 128 == 0 && stage_bytes % 128 == 0, "copies start on 128-byte boundaries");
 };
 // Of a group of four tokens, with the norms and the scale in them.
 struct GdrGroup {
@@ -225,13 +237,15 @@ struct GdrGroup {
 
 template <typename T, int N, int RPT>
 __global__ void __launch_bounds__(kGdrTokThreads)
-gdr_tokens_kernel(const GdrParams p)
+gdr_tokens_kernel(const GdrParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v)
 {
     using Lay = GdrTokensLayout<T, N, RPT>;
     constexpr int M = N / 32;
     constexpr int kRows = Lay::rows;
-    __shared__ __align__(16) unsigned char ring[Lay::stages * Lay::stage_bytes];
+    __shared__ __align__(128) unsigned char ring[Lay::stages * Lay::stage_bytes];
     __shared__ __align__(16) GdrGroup coef[2][2];
+    __shared__ uint64_t full[Lay::stages];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int e = lane & 7, sub = lane >> 3;
     const int tiles = p.P / kRows;
@@ -242,31 +256,27 @@ gdr_tokens_kernel(const GdrParams p)
 
     const int64_t t_first = static_cast<int64_t>(b) * p.L;
     const int L = static_cast<int>(p.L), blocks = (L + kGdrBlock - 1) / kGdrBlock;
+    if (tid == 0) {
+        for (int i = 0; i < Lay::stages; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
     auto slot = [&](int blk) { return ring + blk % Lay::stages * Lay::stage_bytes; };
 
     if (warp >= kGdrRecThreads / 32) {
-        const T* kp = static_cast<const T*>(p.k) + t_first * p.k_stride + g * N;
-        const T* qp = static_cast<const T*>(p.q) + t_first * p.q_stride + g * N;
-        const T* vp = static_cast<const T*>(p.v) + t_first * p.v_stride + static_cast<int64_t>(h) * p.P + first;
         const int half = warp - kGdrRecThreads / 32;
-        // this warp's group of a block: four tokens of k, q and v in 16-byte pieces
+        // a block: one tensor copy each for k, q and v, zeros past the sequence
         auto request = [&](int blk) {
-            if (blk < blocks) {
-                unsigned char* st = slot(blk);
-                constexpr int el = 16 / sizeof(T), nk = N / el, nv = kRows / el, per = 2 * nk + nv;
-#pragma unroll 2
-                for (int i = lane; i < kGdrGroup * per; i += 32) {
-                    const int t = half * kGdrGroup + i / per, c = i % per;
-                    const int64_t at = blk * kGdrBlock + t;
-                    const bool in_k = c < nk, in_q = c < 2 * nk;
-                    const int col = (in_k ? c : in_q ? c - nk : c - 2 * nk) * el;
-                    unsigned char* dst = st + (in_k ? Lay::k_off : in_q ? Lay::q_off : Lay::v_off) +
-                                         (t * (in_q ? N : kRows) + col) * sizeof(T);
-                    if (at < L) cp_async16(dst, (in_k ? kp : in_q ? qp : vp) + at * (in_k ? p.k_stride : in_q ? p.q_stride : p.v_stride) + col);
-                    else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);       // past the sequence
-                }
-            }
-            cp_async_commit();
+            if (blk >= blocks || tid != kGdrRecThreads) return;
+            unsigned char* st = slot(blk);
+            uint64_t* bar = &full[blk % Lay::stages];
+            mbar_arrive_expect_tx(bar, Lay::stage_bytes);
+            tma_load_3d(st + Lay::k_off, &tm_k, g * N, blk * kGdrBlock, b, bar);
+            tma_load_3d(st + Lay::q_off, &tm_q, g * N, blk * kGdrBlock, b, bar);
+            tma_load_3d(st + Lay::v_off, &tm_v, h * p.P + first, blk * kGdrBlock, b, bar);
+        };
+        auto landed = [&](int blk, unsigned limit) {
+            return warp_wait(&full[blk % Lay::stages], static_cast<unsigned>((blk / Lay::stages) & 1), limit);
         };
         // lanes 0..3: dt and beta of the group's tokens
         const T* dtp = static_cast<const T*>(p.dt) + (t_first + half * kGdrGroup + lane) * p.H + h;
@@ -341,16 +351,23 @@ gdr_tokens_kernel(const GdrParams p)
         request(0);
         request(1);
         fetch_gates(0);
-        cp_async_wait<1>();
-        asm volatile("bar.sync 1, 64;\n" ::: "memory");       // the other helper's copies of the block too
+        bool ok = landed(0, p.wait_limit);
         work_out(0);
         fetch_gates(1);
         for (int blk = 0; blk < blocks; ++blk) {
-            cp_async_wait<0>();
+            if (blk + 1 < blocks) ok = landed(blk + 1, p.wait_limit) && ok;
             __syncthreads();      // block blk + 1 is there, blk's coefficients are, blk - 1 is done with
             request(blk + 2);
             if (blk + 1 < blocks) work_out(blk + 1);
             fetch_gates(blk + 2);
+        }
+        if (!ok) {
+            // the copies in flight finish before their shared memory goes away
+            for (int blk = max(0, blocks - Lay::stages); blk < blocks; ++blk) landed(blk, 1u << 20);
+            if (lane == 0) {
+                atomicOr(&g_mm_fault, 1u);
+                if (p.status) atomicExch(p.status, (p.status_epoch << 8) | 1ull);
+            }
         }
         return;
     }
@@ -552,11 +569,6 @@ __device__ __forceinline__ bool elect_sync() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
     return p != 0;
 }
-// the same answer for every lane of the warp
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned limit) {
-    return __all_sync(kFull, mbar_wait_bounded(bar, parity, limit));
-}
-
 template <int N>
 struct GdrPrepLayout {
     static constexpr int ld = kGdrC + 4;                          // fp32 rows, 16-byte pieces of 8 rows on different banks
@@ -924,12 +936,6 @@ struct GdrScanLayout {
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" :: "r"(smem_addr(bar)) : "memory");
-}
-// One contiguous bulk copy global -> shared (16-byte aligned, a multiple of 16
-// bytes), completion on `bar`.
-__device__ __forceinline__ void bulk_load(void* dst, const void* gsrc, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n"
-                 :: "r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(bytes), "r"(smem_addr(bar)) : "memory");
 }
 // 16 consecutive fp32 columns of this thread's row of tensor memory, without
 // waiting: the registers are valid after tmem_wait_ld

@@ -1936,11 +1936,43 @@ mm::GdrParams gdr_params(const GdrArgs& a) {
     return p;
 }
 
-// kern: RPT state rows a lane of its 128 threads that hold the state
+// 3-D map over the rows of q, k or v: [batch][tokens][cols], tokens `stride`
+// elements apart, boxes of rows x box_cols.
+bool encode_gdr_rows(CUtensorMap* m, const void* base, bool bf16, int64_t cols, int64_t stride, int64_t seqlen, int64_t batch,
+                     int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int64_t es = bf16 ? 2 : 4;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(seqlen), static_cast<cuuint64_t>(batch)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride * es), static_cast<cuuint64_t>(seqlen * stride * es)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims,
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// RPT: state rows a lane of the 128 threads that hold the state
+template <int RPT>
+dim3 gdr_rows_grid(const mm::GdrParams& p, int64_t batch) {
+    return dim3(static_cast<unsigned>(p.H * (p.P / (mm::kGdrRecThreads / 8 * RPT))), static_cast<unsigned>(batch));
+}
 template <typename T, int N, int RPT>
-cudaError_t launch_gdr_rows(const mm::GdrParams& p, int64_t batch, cudaStream_t s, void (*kern)(mm::GdrParams), int threads) {
-    const dim3 grid(static_cast<unsigned>(p.H * (p.P / (mm::kGdrRecThreads / 8 * RPT))), static_cast<unsigned>(batch));
-    kern<<<grid, threads, forced_launch_failure() ? (1 << 20) : 0, s>>>(p);
+cudaError_t launch_gdr_tokens(const mm::GdrParams& p, int64_t batch, cudaStream_t s) {
+    CUtensorMap tq, tk, tv;
+    constexpr bool bf16 = sizeof(T) == 2;
+    constexpr int rows = mm::GdrTokensLayout<T, N, RPT>::rows;
+    if (!encode_gdr_rows(&tq, p.q, bf16, p.G * N, p.q_stride, p.L, batch, N, mm::kGdrBlock, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_gdr_rows(&tk, p.k, bf16, p.G * N, p.k_stride, p.L, batch, N, mm::kGdrBlock, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_gdr_rows(&tv, p.v, bf16, p.H * p.P, p.v_stride, p.L, batch, rows, mm::kGdrBlock, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    mm::gdr_tokens_kernel<T, N, RPT><<<gdr_rows_grid<RPT>(p, batch), mm::kGdrTokThreads, forced_launch_failure() ? (1 << 20) : 0, s>>>(
+        p, tq, tk, tv);
+    return cudaGetLastError();
+}
+template <typename T, int N, int RPT>
+cudaError_t launch_gdr_one(const mm::GdrParams& p, int64_t batch, cudaStream_t s) {
+    mm::gdr_recurrent_kernel<T, N, RPT><<<gdr_rows_grid<RPT>(p, batch), mm::kGdrRecThreads, forced_launch_failure() ? (1 << 20) : 0, s>>>(p);
     return cudaGetLastError();
 }
 // State rows per lane: more once the grid fills the SMs with them (fewer
@@ -1948,11 +1980,8 @@ cudaError_t launch_gdr_rows(const mm::GdrParams& p, int64_t batch, cudaStream_t 
 template <typename T, int N>
 cudaError_t launch_gdr_recurrent_n(const mm::GdrParams& p, int64_t batch, cudaStream_t s) {
     const int64_t rows = batch * p.H * p.P / (mm::kGdrRecThreads / 8);        // CTAs of one row a lane
-    if (p.L > 1)
-        return rows >= 16 * plan_sms() ? launch_gdr_rows<T, N, 2>(p, batch, s, mm::gdr_tokens_kernel<T, N, 2>, mm::kGdrTokThreads)
-                                       : launch_gdr_rows<T, N, 1>(p, batch, s, mm::gdr_tokens_kernel<T, N, 1>, mm::kGdrTokThreads);
-    return rows >= 16 * plan_sms() ? launch_gdr_rows<T, N, 4>(p, batch, s, mm::gdr_recurrent_kernel<T, N, 4>, mm::kGdrRecThreads)
-                                   : launch_gdr_rows<T, N, 1>(p, batch, s, mm::gdr_recurrent_kernel<T, N, 1>, mm::kGdrRecThreads);
+    if (p.L > 1) return rows >= 16 * plan_sms() ? launch_gdr_tokens<T, N, 2>(p, batch, s) : launch_gdr_tokens<T, N, 1>(p, batch, s);
+    return rows >= 16 * plan_sms() ? launch_gdr_one<T, N, 4>(p, batch, s) : launch_gdr_one<T, N, 1>(p, batch, s);
 }
 mm_status launch_gdr_recurrent(const mm::GdrParams& p, const GdrArgs& a, cudaStream_t s) {
     cudaError_t e;
@@ -1964,13 +1993,15 @@ mm_status launch_gdr_recurrent(const mm::GdrParams& p, const GdrArgs& a, cudaStr
     return e == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
-// The chunked form: bf16 calls of at least kGdrChunkedMin tokens whose copies'
-// coordinates and strides fit (a workspace row index in 31 bits, a tensor's
-// strides in 40).  The chunks run in rounds of as many as bring the workspace
+// The chunked form: bf16 calls of enough tokens.  One chunk costs 13 us (two
+// dependent kernels, the triangular system between them); token by token, a
+// block of 8 tokens costs 1.3 to 2.2 us while the state's rows leave the SMs
+// free (crossing at 41 to 62 tokens), 14 us with 32768 rows of 128 (at 11).  The chunks run in rounds of as many as bring the workspace
 // to kGdrRoundUnits chunks of a head, each round from the state that the one
 // before left in the workspace (two of them in turn: a round's first segment
 // reads one while its last writes the other).
-constexpr int64_t kGdrChunkedMin = 24;
+constexpr int64_t kGdrManyRows = 16384;        // state rows of all heads
+int64_t gdr_chunked_min(int64_t rows) { return rows >= kGdrManyRows ? 16 : 44; }
 constexpr int64_t kGdrRoundUnits = 16384;      // 33 KB each
 struct GdrPlan {
     bool chunked = false;
@@ -2001,7 +2032,7 @@ int gdr_segments(int64_t batch, int64_t tiles, int64_t trans_tiles, int64_t chun
 }
 GdrPlan plan_gdr(int64_t batch, int64_t seqlen, int64_t heads, int64_t headdim, int64_t d_state, mm_dtype act, int64_t sms) {
     GdrPlan pl;
-    if (act != MM_BF16 || seqlen < kGdrChunkedMin || batch * heads > (int64_t(1) << 20)) return pl;
+    if (act != MM_BF16 || seqlen < gdr_chunked_min(batch * heads * headdim) || batch * heads > (int64_t(1) << 20)) return pl;
     pl.chunked = true;
     pl.chunks = (seqlen + mm::kGdrC - 1) / mm::kGdrC;
     pl.round = std::min(pl.chunks, std::max<int64_t>(1, kGdrRoundUnits / (batch * heads)));
@@ -2015,20 +2046,6 @@ GdrPlan plan_gdr(int64_t batch, int64_t seqlen, int64_t heads, int64_t headdim, 
     pl.off_carry = pl.off_in + static_cast<size_t>(rows * headdim) * 4;
     pl.total = pl.off_carry + (pl.round < pl.chunks ? static_cast<size_t>(batch * heads * headdim * d_state) * 8 : 0);
     return pl;
-}
-
-// 3-D map over the rows of q, k or v: [batch][tokens][cols], tokens `stride`
-// elements apart, boxes of 64 tokens x 64 columns in the 128-byte swizzle.
-bool encode_gdr_rows(CUtensorMap* m, const void* base, int64_t cols, int64_t stride, int64_t seqlen, int64_t batch) {
-    auto enc = tensor_map_encoder();
-    if (!enc) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(seqlen), static_cast<cuuint64_t>(batch)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride * 2), static_cast<cuuint64_t>(seqlen * stride * 2)};
-    const cuuint32_t box[3] = {64, mm::kGdrC, 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A launch that may start while the kernel before it in the stream still runs
@@ -2051,9 +2068,12 @@ cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, int threads, si
 template <int N>
 mm_status launch_gdr_chunked(const GdrArgs& a, const GdrPlan& pl, unsigned char* w, unsigned long long epoch, cudaStream_t s) {
     CUtensorMap tq, tk, tv, tt;
-    if (!encode_gdr_rows(&tq, a.q, a.groups * N, a.q_stride, a.seqlen, a.batch) ||
-        !encode_gdr_rows(&tk, a.k, a.groups * N, a.k_stride, a.seqlen, a.batch) ||
-        !encode_gdr_rows(&tv, a.v, a.heads * a.headdim, a.v_stride, a.seqlen, a.batch) ||
+    // operand tiles: 64 tokens x 64 columns in the products' 128-byte swizzle
+    auto tile_map = [&](CUtensorMap* m, const void* base, int64_t cols, int64_t stride) {
+        return encode_gdr_rows(m, base, true, cols, stride, a.seqlen, a.batch, 64, mm::kGdrC, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    if (!tile_map(&tq, a.q, a.groups * N, a.q_stride) || !tile_map(&tk, a.k, a.groups * N, a.k_stride) ||
+        !tile_map(&tv, a.v, a.heads * a.headdim, a.v_stride) ||
         !encode_gemm_2d(&tt, w + pl.off_t, 64, a.batch * a.heads * pl.round * 256, 64))
         return MM_ERR_CUDA;
     static std::atomic<unsigned long long> allowed_prep{0}, allowed_scan{0}, allowed_state{0}, allowed_segment{0};
@@ -2155,6 +2175,7 @@ mm_status mamba_gdr_fwd(const void* q, const void* k, const void* v, const void*
     mm::GdrParams p = gdr_params(a);
     p.status = static_cast<unsigned long long*>(workspace);
     p.status_epoch = epoch;
+    p.wait_limit = copy_wait_limit();
     return launch_gdr_recurrent(p, a, static_cast<cudaStream_t>(stream));
 }
 
