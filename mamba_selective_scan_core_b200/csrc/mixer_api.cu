@@ -2211,7 +2211,7 @@ bool encode_q4_2d(CUtensorMap* m, const void* base, bool bytes, int64_t cols, in
     const cuuint32_t estr[2] = {1, 1};
     return enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int GB, int MT, bool ZEROS, bool OUT_BF16>
@@ -2222,7 +2222,8 @@ cudaError_t launch_q4_t(mm::Q4Params p, const void* x, const void* W, cudaStream
     auto kern = mm::proj_q4_kernel<GB, MT, ZEROS, OUT_BF16>;
     static std::atomic<unsigned long long> smem_allowed{0};
     if (cudaError_t e = allow_smem(kern, smem_allowed); e != cudaSuccess) return e;
-    // K is split over a cluster until the grid covers the SMs or a CTA has two slots
+    // K is split over a cluster until the grid covers the SMs or a CTA has two
+    // slots (three CTAs a SM took 16.2 us where this takes 14.7: 16384 x 4096)
     const int64_t tiles = (static_cast<int64_t>(p.N) + mm::kQ4Rows - 1) / mm::kQ4Rows * ((p.M + MT * 8 - 1) / (MT * 8));
     const int slots = (p.K + mm::kQ4K - 1) / mm::kQ4K;
     int split = 1;

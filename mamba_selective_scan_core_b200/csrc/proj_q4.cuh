@@ -57,7 +57,7 @@ struct Q4Layout {
     static constexpr int w_bytes = kQ4Rows * 128;                // 8 KB
     static constexpr int x_box = MT * 8 * 128;                   // 64 inputs of the rows of x
     static constexpr int stage_bytes = w_bytes + 4 * x_box;
-    static constexpr int stages = MT <= 2 ? 6 : MT == 4 ? 5 : 4;
+    static constexpr int stages = 4;
     static constexpr int red_ld = kQ4Rows + 1;
     static constexpr int red_bytes = 2 * MT * 8 * red_ld * 4;    // both halves' sums, over the ring once it is drained
     static constexpr int smem_bytes = 1024 + stages * stage_bytes + 2 * stages * 8 + 16;
@@ -65,26 +65,37 @@ struct Q4Layout {
 };
 
 __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};\n"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// the bf16 pair (c_i - 8, c_{i+4} - 8) of a packed word already shifted by 4 i
-__device__ __forceinline__ uint32_t q4_pair(uint32_t w) {
-    const uint32_t v = (w & 0x000f000fu) | 0x43004300u;
+// the bf16 pair (c_i - 8, c_{i+4} - 8) of a packed word already shifted by 4 i;
+// `magic` is 0x43004300 in a register: with both constants immediate the mask
+// and the or are two instructions, and these bound the kernel
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w, uint32_t magic) {
+    uint32_t v;
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;\n" : "=r"(v) : "r"(w), "r"(magic));
     __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __floats2bfloat162_rn(136.0f, 136.0f));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
+// n words (1, 2 or 4) at an address aligned to as many.  Plain loads, which
+// the compiler moves between the products as it sees fit.
+template <int n>
+__device__ __forceinline__ void load_words(const unsigned char* p, uint32_t (&v)[n]) {
+    if constexpr (n == 4) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p);
+        v[0] = w.x;
+        v[1] = w.y;
+        v[2] = w.z;
+        v[3] = w.w;
+    } else if constexpr (n == 2) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
+        v[0] = w.x;
+        v[1] = w.y;
+    } else {
+        v[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -168,89 +179,106 @@ proj_q4_kernel(const Q4Params p, const __grid_constant__ CUtensorMap tm_w, const
         }
     } else {
         constexpr int kGroups = 4 / GB;               // groups of a warp's 128 inputs
+        uint32_t magic = 0x43004300u;
+        asm volatile("" : "+r"(magic));               // kept in its register
         const int groups = p.K / (32 * GB);
         // this lane's two outputs; outputs past N read the last one's scales (their sums are not stored)
         const int64_t r0 = static_cast<int64_t>(min(n0 + rt * 16 + g, p.N - 1)) * groups;
         const int64_t r1 = static_cast<int64_t>(min(n0 + rt * 16 + g + 8, p.N - 1)) * groups;
-        float sc[2][kGroups], zc[2][kGroups];
-        auto fetch = [&](int i) {
+        // Scales and zero points come straight from memory, two slots ahead.
+        constexpr int kAhead = 2;
+        __nv_bfloat16 sc[kAhead][2][kGroups], zc[kAhead][2][kGroups];
+        const __nv_bfloat16 none = __float2bfloat16_rn(0.0f);
+        constexpr int kStep = kQ4K / (32 * GB);        // groups of a slot
+        const int g0 = slot0 * kStep + kh * kGroups;
+        const __nv_bfloat16 *sp0 = p.scales + r0 + g0, *sp1 = p.scales + r1 + g0;
+        const __nv_bfloat16 *zp0 = p.zeros + r0 + g0, *zp1 = p.zeros + r1 + g0;
+        auto fetch = [&](int i, int d) {
+            const int left = i < slots ? groups - g0 - i * kStep : 0;     // groups from this one on
 #pragma unroll
             for (int q = 0; q < kGroups; ++q) {
-                const int gi = ((slot0 + i) * kQ4K + kh * 128) / (32 * GB) + q;
-                const bool in = gi < groups;
-                sc[0][q] = in ? __bfloat162float(p.scales[r0 + gi]) : 0.0f;
-                sc[1][q] = in ? __bfloat162float(p.scales[r1 + gi]) : 0.0f;
+                const bool in = q < left;
+                sc[d][0][q] = in ? sp0[i * kStep + q] : none;
+                sc[d][1][q] = in ? sp1[i * kStep + q] : none;
                 if constexpr (ZEROS) {
-                    zc[0][q] = in ? 8.0f - __bfloat162float(p.zeros[r0 + gi]) : 0.0f;
-                    zc[1][q] = in ? 8.0f - __bfloat162float(p.zeros[r1 + gi]) : 0.0f;
+                    zc[d][0][q] = in ? zp0[i * kStep + q] : none;
+                    zc[d][1][q] = in ? zp1[i * kStep + q] : none;
                 }
             }
         };
-        if (slots > 0) fetch(0);
-        for (int i = 0; i < slots; ++i) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) fetch(d, d);
+        for (int i0 = 0; i0 < slots && ok; i0 += kAhead)
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+            const int i = i0 + d;
+            if (i >= slots) break;
             const int s = i % Lay::stages;
             float s0[kGroups], s1[kGroups], z0[kGroups], z1[kGroups];
 #pragma unroll
             for (int q = 0; q < kGroups; ++q) {
-                s0[q] = sc[0][q];
-                s1[q] = sc[1][q];
-                z0[q] = ZEROS ? zc[0][q] : 0.0f;
-                z1[q] = ZEROS ? zc[1][q] : 0.0f;
+                s0[q] = __bfloat162float(sc[d][0][q]);
+                s1[q] = __bfloat162float(sc[d][1][q]);
+                z0[q] = ZEROS ? 8.0f - __bfloat162float(zc[d][0][q]) : 0.0f;
+                z1[q] = ZEROS ? 8.0f - __bfloat162float(zc[d][1][q]) : 0.0f;
             }
-            if (i + 1 < slots) fetch(i + 1);
+            fetch(i + kAhead, d);
             if (!mbar_wait_bounded(&full[s], static_cast<unsigned>((i / Lay::stages) & 1), p.wait_limit)) {
                 ok = false;
                 break;
             }
-            const uint32_t wrow = smem_addr(sm + s * Lay::stage_bytes) + (rt * 16 + g) * 128 + c * 4;
-            const uint32_t xrow = smem_addr(sm + s * Lay::stage_bytes + Lay::w_bytes) + g * 128;
-            float part[MT][4], xs[MT][4];
+            // Lane c takes GB consecutive words of a group of a row (one load),
+            // eight inputs each: as long as x comes in the same order, a
+            // product's inputs may be any of the group's.
+            const unsigned char* wrow = sm + s * Lay::stage_bytes + (rt * 16 + g) * 128;
+            const unsigned char* xrow = sm + s * Lay::stage_bytes + Lay::w_bytes + g * 128;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int kb = kh * 4 + j;
-                if (j % GB == 0) {
+            for (int q = 0; q < kGroups; ++q) {
+                const int word0 = kh * 16 + q * 4 * GB + c * GB;        // of the row's 32
+                const uint32_t woff = ((static_cast<uint32_t>(word0 >> 2) ^ g) << 4) + (word0 & 3) * 4;
+                uint32_t w0[GB], w1[GB];
+                load_words<GB>(wrow + woff, w0);
+                load_words<GB>(wrow + 8 * 128 + woff, w1);
+                float part[MT][4], xs[MT][4];
 #pragma unroll
-                    for (int t = 0; t < MT; ++t)
+                for (int t = 0; t < MT; ++t)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) part[t][q] = xs[t][q] = 0.0f;
-                }
-                const uint32_t woff = static_cast<uint32_t>((kb ^ g) << 4);
-                const uint32_t w0 = lds32(wrow + woff), w1 = lds32(wrow + 8 * 128 + woff);
-                uint32_t a[2][4];
+                    for (int k = 0; k < 4; ++k) part[t][k] = xs[t][k] = 0.0f;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    a[u][0] = q4_pair(w0 >> (8 * u));
-                    a[u][1] = q4_pair(w1 >> (8 * u));
-                    a[u][2] = q4_pair(w0 >> (8 * u + 4));
-                    a[u][3] = q4_pair(w1 >> (8 * u + 4));
-                }
-                const uint32_t xoff = (kb >> 1) * Lay::x_box + static_cast<uint32_t>((((kb & 1) * 4 + c) ^ g) << 4);
+                for (int j = 0; j < GB; ++j) {
+                    uint32_t a[2][4];
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    const uint4 x = lds128(xrow + t * 1024 + xoff);
-                    const uint32_t b0 = __byte_perm(x.x, x.z, 0x5410), b1 = __byte_perm(x.x, x.z, 0x7632);
-                    const uint32_t b2 = __byte_perm(x.y, x.w, 0x5410), b3 = __byte_perm(x.y, x.w, 0x7632);
-                    mma_bf16_16816(part[t], a[0], b0, b1);
-                    mma_bf16_16816(part[t], a[1], b2, b3);
-                    if constexpr (ZEROS) {
-                        constexpr uint32_t one = 0x3f803f80u;
-                        const uint32_t ones[4] = {one, one, one, one};
-                        mma_bf16_16816(xs[t], ones, b0, b1);
-                        mma_bf16_16816(xs[t], ones, b2, b3);
+                    for (int u = 0; u < 2; ++u) {
+                        a[u][0] = q4_pair(w0[j] >> (8 * u), magic);
+                        a[u][1] = q4_pair(w1[j] >> (8 * u), magic);
+                        a[u][2] = q4_pair(w0[j] >> (8 * u + 4), magic);
+                        a[u][3] = q4_pair(w1[j] >> (8 * u + 4), magic);
                     }
-                }
-                if (j % GB == GB - 1) {
-                    constexpr int dq = GB;
-                    const int q = j / dq;
+                    const int word = word0 + j;      // its eight inputs: a 16-byte piece of x
+                    const uint32_t xoff = (word >> 3) * Lay::x_box + ((static_cast<uint32_t>(word & 7) ^ g) << 4);
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float v0 = ZEROS ? fmaf(z0[q], xs[t][e], part[t][e]) : part[t][e];
-                            const float v1 = ZEROS ? fmaf(z1[q], xs[t][e], part[t][2 + e]) : part[t][2 + e];
-                            acc[t][e] = fmaf(s0[q], v0, acc[t][e]);
-                            acc[t][2 + e] = fmaf(s1[q], v1, acc[t][2 + e]);
+                        const uint4 x = *reinterpret_cast<const uint4*>(xrow + t * 1024 + xoff);
+                        const uint32_t b0 = __byte_perm(x.x, x.z, 0x5410), b1 = __byte_perm(x.x, x.z, 0x7632);
+                        const uint32_t b2 = __byte_perm(x.y, x.w, 0x5410), b3 = __byte_perm(x.y, x.w, 0x7632);
+                        mma_bf16_16816(part[t], a[0], b0, b1);
+                        mma_bf16_16816(part[t], a[1], b2, b3);
+                        if constexpr (ZEROS) {
+                            constexpr uint32_t one = 0x3f803f80u;
+                            const uint32_t ones[4] = {one, one, one, one};
+                            mma_bf16_16816(xs[t], ones, b0, b1);
+                            mma_bf16_16816(xs[t], ones, b2, b3);
                         }
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float v0 = ZEROS ? fmaf(z0[q], xs[t][e], part[t][e]) : part[t][e];
+                        const float v1 = ZEROS ? fmaf(z1[q], xs[t][e], part[t][2 + e]) : part[t][2 + e];
+                        acc[t][e] = fmaf(s0[q], v0, acc[t][e]);
+                        acc[t][2 + e] = fmaf(s1[q], v1, acc[t][2 + e]);
                     }
                 }
             }
