@@ -829,6 +829,17 @@ class _Torch:
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda i: torch.cuda.current_stream(i).cuda_stream)
         self.lib = lib()
+        # the same calls with the tensors looked at in C++ (they return None
+        # where the Python below is to decide); without the module, this alone
+        try:
+            from . import _calls
+        except ImportError:
+            self.calls = None
+        else:
+            _calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                self.lib.mamba_gdr_fwd, self.lib.mamba_gdr_workspace_size, self.lib.mamba_gdr_state_update,
+                self.lib.mamba_proj_q4)))
+            self.calls = _calls
 
 
 _torch_names = None
@@ -855,6 +866,10 @@ def gdr_fwd(q, k, v, dt, beta, dt_bias, A, h0=None, *, scale=None, norm_eps=1e-6
     when it is 0.  Returns (y [B,L,H,P], h_last [B,H,P,N] fp32), allocating any
     output not given."""
     T = _torch_names or _names()
+    if stream is None and T.calls is not None:
+        out = T.calls.gdr_fwd(q, k, v, dt, beta, dt_bias, A, h0, scale, norm_eps, y, h_last, workspace)
+        if out is not None:
+            return out
     f32, dtype, idx = T.f32, v.dtype, v.get_device()
     act = T.codes.get(dtype)
     if act is None:
@@ -932,6 +947,10 @@ def gdr_state_update(q, k, v, dt, beta, dt_bias, A, state, *, scale=None, norm_e
     spaced), dt and beta [B,H], dt_bias/A [H] fp32 (dt_bias may be None).  scale
     and norm_eps as gdr_fwd.  Returns y [B,H,P], allocated if not given."""
     T = _torch_names or _names()
+    if stream is None and T.calls is not None:
+        out = T.calls.gdr_state_update(q, k, v, dt, beta, dt_bias, A, state, scale, norm_eps, y)
+        if out is not None:
+            return out
     f32, dtype, idx = T.f32, v.dtype, v.get_device()
     act = T.codes.get(dtype)
     if act is None:
@@ -986,12 +1005,16 @@ def proj_q4(x, W, scales, zeros=None, *, group=128, out=None, out_dtype=None, st
     and zeros [N,K/group] bf16 (zeros None: 8), weight = scale (number - zero).
     out [M,N] fp32 (default) or bf16, allocated if not given."""
     T = _torch_names or _names()
+    dtype = out_dtype or (out.dtype if out is not None else T.f32)
+    if stream is None and T.calls is not None and dtype in T.codes:
+        made = T.calls.proj_q4(x, W, scales, zeros, group, out, dtype is T.bf16)
+        if made is not None:
+            return made
     bf, idx = T.bf16, x.get_device()
     M, K = x.shape
     N = W.shape[0]
     if group <= 0:
         raise ValueError(f"group must be positive, got {group}")
-    dtype = out_dtype or (out.dtype if out is not None else T.f32)
     code = T.codes.get(dtype)
     if code is None:
         _act_code(dtype)

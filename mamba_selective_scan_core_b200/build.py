@@ -1,7 +1,8 @@
 """Compile the CUDA library (sm_100a) in-tree: libmamba_mixer.so next to this
 file, and its checked build libmamba_mixer_checked.so (compiled with
 MM_CHECK_BOUNDS: the forward and decode kernels check every index they form
-against its buffer, skip an access outside it and report MM_ERR_BOUNDS).
+against its buffer, skip an access outside it and report MM_ERR_BOUNDS); and
+the Python module of the calls a decoded token makes, _calls.so.
 
     python -m mamba_selective_scan_core_b200.build [--force] [--verbose] [--checked]
 """
@@ -21,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 SOURCE = os.path.join(CSRC, "mixer_api.cu")
 LIB_PATH = os.path.join(PKG, "libmamba_mixer.so")
 CHECKED_LIB_PATH = os.path.join(PKG, "libmamba_mixer_checked.so")
+CALLS_SOURCE = os.path.join(CSRC, "calls.cpp")
+CALLS_PATH = os.path.join(PKG, "_calls.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -57,7 +60,31 @@ def _compile(path: str, flags, verbose: bool) -> str:
     return path
 
 
+def build_calls(force: bool = False, verbose: bool = False) -> str:
+    """The module of calls.cpp, against the torch and Python that run this."""
+    newest = max(os.path.getmtime(f) for f in (CALLS_SOURCE, os.path.join(INCLUDE, "mamba_mixer.h")))
+    if not force and os.path.exists(CALLS_PATH) and os.path.getmtime(CALLS_PATH) >= newest:
+        return CALLS_PATH
+    import sysconfig
+
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+           CALLS_SOURCE, "-o", tmp, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, CALLS_PATH)
+    return CALLS_PATH
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    build_calls(force, verbose)
     if not force and not stale(LIB_PATH):
         return LIB_PATH
     return _compile(LIB_PATH, list(extra_flags), verbose)
