@@ -79,23 +79,10 @@ __device__ __forceinline__ uint32_t q4_pair(uint32_t w, uint32_t magic) {
     __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __floats2bfloat162_rn(136.0f, 136.0f));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
-// n words (1, 2 or 4) at an address aligned to as many.  Plain loads, which
-// the compiler moves between the products as it sees fit.
-template <int n>
-__device__ __forceinline__ void load_words(const unsigned char* p, uint32_t (&v)[n]) {
-    if constexpr (n == 4) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
-        v[0] = w.x;
-        v[1] = w.y;
-        v[2] = w.z;
-        v[3] = w.w;
-    } else if constexpr (n == 2) {
-        const uint2 w = *reinterpret_cast<const uint2*>(p);
-        v[0] = w.x;
-        v[1] = w.y;
-    } else {
-        v[0] = *reinterpret_cast<const uint32_t*>(p);
-    }
+__device__ __forceinline__ void load_pair(const unsigned char* p, uint32_t* v) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    v[0] = w.x;
+    v[1] = w.y;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -236,9 +223,24 @@ proj_q4_kernel(const Q4Params p, const __grid_constant__ CUtensorMap tm_w, const
             for (int q = 0; q < kGroups; ++q) {
                 const int word0 = kh * 16 + q * 4 * GB + c * GB;        // of the row's 32
                 const uint32_t woff = ((static_cast<uint32_t>(word0 >> 2) ^ g) << 4) + (word0 & 3) * 4;
+                // with four words a lane, lanes 2 and 3 take theirs in the order
+                // 2, 3, 0, 1: x's pieces of eight lanes then lie in eight
+                // different 16-byte columns
+                const int turn = GB == 4 ? c & 2 : 0;
                 uint32_t w0[GB], w1[GB];
-                load_words<GB>(wrow + woff, w0);
-                load_words<GB>(wrow + 8 * 128 + woff, w1);
+                if constexpr (GB == 4) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        load_pair(wrow + woff + ((2 * k) ^ turn) * 4, w0 + 2 * k);
+                        load_pair(wrow + 8 * 128 + woff + ((2 * k) ^ turn) * 4, w1 + 2 * k);
+                    }
+                } else if constexpr (GB == 2) {
+                    load_pair(wrow + woff, w0);
+                    load_pair(wrow + 8 * 128 + woff, w1);
+                } else {
+                    w0[0] = *reinterpret_cast<const uint32_t*>(wrow + woff);
+                    w1[0] = *reinterpret_cast<const uint32_t*>(wrow + 8 * 128 + woff);
+                }
                 float part[MT][4], xs[MT][4];
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
@@ -254,7 +256,7 @@ proj_q4_kernel(const Q4Params p, const __grid_constant__ CUtensorMap tm_w, const
                         a[u][2] = q4_pair(w0[j] >> (8 * u + 4), magic);
                         a[u][3] = q4_pair(w1[j] >> (8 * u + 4), magic);
                     }
-                    const int word = word0 + j;      // its eight inputs: a 16-byte piece of x
+                    const int word = word0 + (j ^ turn);      // its eight inputs: a 16-byte piece of x
                     const uint32_t xoff = (word >> 3) * Lay::x_box + ((static_cast<uint32_t>(word & 7) ^ g) << 4);
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
