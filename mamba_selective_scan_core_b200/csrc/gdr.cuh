@@ -352,18 +352,23 @@ gdr_tokens_kernel(const GdrParams p, const __grid_constant__ CUtensorMap tm_q, c
         request(1);
         fetch_gates(0);
         bool ok = landed(0, p.wait_limit);
+        int asked = min(2, blocks);       // blocks requested: no more once a wait has given up
         work_out(0);
         fetch_gates(1);
         for (int blk = 0; blk < blocks; ++blk) {
-            if (blk + 1 < blocks) ok = landed(blk + 1, p.wait_limit) && ok;
+            if (ok && blk + 1 < blocks) ok = landed(blk + 1, p.wait_limit);
             __syncthreads();      // block blk + 1 is there, blk's coefficients are, blk - 1 is done with
-            request(blk + 2);
+            if (ok && blk + 2 < blocks) {
+                request(blk + 2);
+                asked = blk + 3;
+            }
             if (blk + 1 < blocks) work_out(blk + 1);
             fetch_gates(blk + 2);
         }
         if (!ok) {
             // the copies in flight finish before their shared memory goes away
-            for (int blk = max(0, blocks - Lay::stages); blk < blocks; ++blk) landed(blk, 1u << 20);
+            if (warp == kGdrRecThreads / 32)
+                for (int blk = max(0, asked - Lay::stages); blk < asked; ++blk) landed(blk, 1u << 20);
             if (lane == 0) {
                 atomicOr(&g_mm_fault, 1u);
                 if (p.status) atomicExch(p.status, (p.status_epoch << 8) | 1ull);

@@ -224,6 +224,102 @@ def test_step(act, B, G, H, P, N, eps):
 
 
 @pytest.mark.parametrize("act", [BF, F32])
+@pytest.mark.parametrize("L", [2, 3, 4, 6, 8, 9, 16, 17, 31])
+def test_few_tokens(act, L):
+    """Groups of four tokens and blocks of eight that the sequence does not fill."""
+    check(gdr_inputs(2, L, 2, 4, 64, 128 if L % 2 else 64, act, seed=200 + L, h0=L % 3 != 0, packed=L % 2 == 0))
+
+
+@pytest.mark.parametrize("act,L", [(F32, 11), (BF, 7)])
+def test_few_tokens_of_many_rows(act, L):
+    """Enough state rows that a lane holds two of them."""
+    check(gdr_inputs(10, L, 4, 16, 256, 64, act, seed=211))
+
+
+@pytest.mark.parametrize("act,B,L,H,P", [(BF, 2, 20, 2, 64), (F32, 1, 30, 2, 64), (BF, 2, 200, 2, 128), (BF, 1, 2500, 1, 64)])
+def test_forced_wait_timeout_is_reported_and_recoverable(monkeypatch, act, B, L, H, P):
+    """Waits that give up at once, token by token, in chunks and in segments:
+    the call's status and the device's say so, and the next call is right."""
+    inp = gdr_inputs(B, L, 1, H, P, 64, act, seed=220)
+    d = to_cuda(inp)
+    ws = torch.full((mm.gdr_workspace_size(B, L, H, P, 64, 1, mm.MM_F32 if act == F32 else mm.MM_BF16),), 255, dtype=torch.uint8,
+                    device="cuda")
+    assert mm.fault_status(reset=True) == 0
+    monkeypatch.setenv("MAMBA_MIXER_WAIT_LIMIT", "0")
+    fwd(d, workspace=ws)
+    assert mm.check_status(ws) == 11
+    assert mm.fault_status(reset=True) == 11
+    monkeypatch.delenv("MAMBA_MIXER_WAIT_LIMIT")
+    y, h = fwd(d, workspace=ws)
+    assert mm.check_status(ws) == 0 and mm.fault_status() == 0
+    ry, rh = gdr_reference(inp, 64 ** -0.5, 1e-6)
+    close(y, ry, "y")
+    close(h, rh, "h_last")
+
+
+@pytest.mark.parametrize("act", [BF, F32])
+@pytest.mark.parametrize("L", [1, 30, 200])
+def test_both_ways_into_the_library(monkeypatch, act, L):
+    """The C++ calls and the ctypes ones: the same bits, given outputs or not."""
+    names = mm._names()
+    assert names.calls is not None
+    d = to_cuda(gdr_inputs(2, L, 1, 2, 64, 64, act, seed=230, packed=True))
+    one = to_cuda(gdr_inputs(2, None, 1, 2, 64, 64, act, seed=231, packed=True))
+    got = []
+    for calls in (names.calls, None):
+        monkeypatch.setattr(names, "calls", calls)
+        y, h = fwd(d)
+        out = torch.empty_like(y)
+        y2, h2 = fwd(d, y=out, h_last=torch.empty_like(h), scale=64 ** -0.5)
+        assert y2.data_ptr() == out.data_ptr()
+        s = h.clone()
+        got.append((y, h, y2, h2, step(one, s), s))
+    torch.cuda.synchronize()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert torch.equal(got[0][0], got[0][2]) and torch.equal(got[0][1], got[0][3])
+
+
+def test_workspace_given():
+    """One that is too small is not used; one on the host is refused."""
+    d = to_cuda(gdr_inputs(1, 300, 1, 2, 64, 64, seed=240))
+    want = fwd(d)
+    small = torch.full((256,), 7, dtype=torch.uint8, device="cuda")
+    got = fwd(d, workspace=small)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and (small == 7).all()
+    with pytest.raises(ValueError):
+        fwd(d, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+
+
+def test_calls_in_a_chain_without_waiting():
+    """Prefills of three lengths, each from the state of the one before and on
+    one workspace, and steps after them, queued at once: what the same calls
+    give one by one."""
+    lens = (300, 20, 2100)
+    parts = [to_cuda(gdr_inputs(1, n, 1, 2, 128, 128, seed=250 + n)) for n in lens]
+    one = to_cuda(gdr_inputs(1, None, 1, 2, 128, 128, seed=251))
+    ws = torch.empty(max(mm.gdr_workspace_size(1, n, 2, 128, 128, 1) for n in lens), dtype=torch.uint8, device="cuda")
+
+    def chain(wait):
+        h, ys = torch.zeros(1, 2, 128, 128, device="cuda"), []
+        for d in parts:
+            y, h = fwd(dict(d, h0=h), workspace=ws)
+            ys.append(y)
+            if wait:
+                torch.cuda.synchronize()
+        for _ in range(3):
+            ys.append(step(one, h))
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return ys + [h]
+
+    for a, b in zip(chain(True), chain(False)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("act", [BF, F32])
 @pytest.mark.parametrize("cut", [1, 64, 100])
 def test_calls_continue_one_another(act, cut):
     """A prefill, a second one from its state, then single tokens: the whole

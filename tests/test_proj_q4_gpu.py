@@ -128,3 +128,32 @@ def test_binding_refuses():
         mm.proj_q4(d["x"][:, ::2], d["W"][:, :64], d["scales"][:, :2], group=64)
     with pytest.raises(TypeError):
         mm.proj_q4(d["x"], d["W"], d["scales"], group=64, out_dtype=torch.float16)
+
+
+def test_forced_wait_timeout_is_reported_and_recoverable(monkeypatch):
+    inp = q4_inputs(3, 200, 2048, 128, seed=11)
+    d = {k: t.cuda() for k, t in inp.items()}
+    assert mm.fault_status(reset=True) == 0
+    monkeypatch.setenv("MAMBA_MIXER_WAIT_LIMIT", "0")
+    mm.proj_q4(d["x"], d["W"], d["scales"], d["zeros"], group=128)
+    torch.cuda.synchronize()
+    assert mm.fault_status(reset=True) == 11
+    monkeypatch.delenv("MAMBA_MIXER_WAIT_LIMIT")
+    check(inp, 128, F32)
+    assert mm.fault_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_both_ways_into_the_library(monkeypatch, dtype):
+    """The C++ call and the ctypes one: the same bits, a given output or not."""
+    names = mm._names()
+    assert names.calls is not None
+    d = {k: t.cuda() for k, t in q4_inputs(3, 100, 512, 64, seed=12).items()}
+    got = []
+    for calls in (names.calls, None):
+        monkeypatch.setattr(names, "calls", calls)
+        out = torch.empty(3, 100, dtype=dtype, device="cuda")
+        assert mm.proj_q4(d["x"], d["W"], d["scales"], d["zeros"], group=64, out=out) is out
+        got += [out, mm.proj_q4(d["x"], d["W"], d["scales"], d["zeros"], group=64, out_dtype=dtype)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[0], t) for t in got)
