@@ -621,10 +621,11 @@ mm_status mamba_m3_state_update(const void* x, const void* z, const void* dt, co
  * state as it is, whatever finite q, k and v it has; sequences of different
  * lengths run as one batch that way (the padding's y is still written).
  *
- * bf16 calls of more than a few tokens run in chunks of 64 as dense products
- * on the tensor cores, their operands in bf16 parts of 16 bits together, sums
- * and the state in fp32; other calls run token by token in fp32.  Which one is
- * a function of the sizes alone.
+ * bf16 calls of more than some tens of tokens run in chunks of 64 as dense
+ * products on the tensor cores, what they compute of their operands in two or
+ * three bf16 parts (18 or 26 bits), sums and the state in fp32; long ones of few
+ * heads in segments of chunks at once.  Other calls run token by token in fp32.
+ * Which one is a function of the sizes, the type and the SM count alone.
  *
  * Supported: d_state 64 or 128, headdim 64, 128, 192 or 256
  * (MM_ERR_UNSUPPORTED otherwise); heads a multiple of groups, both positive,

@@ -505,10 +505,14 @@ gdr_tokens_kernel(const GdrParams p, const __grid_constant__ CUtensorMap tm_q, c
 // under the key's makes each product 128 rows tall, so the outputs cost no
 // product of their own, and the value of a row of [k; q] S^T or [T; M T] X is
 // in one thread's reach: X, u' and y are elementwise.  The state stays in
-// registers in fp32 (thread: one n, 32 or 16 of the tile's rows).  Operands
-// that the kernels compute (T, M T, S, X, u') are split in two bf16 parts and
-// their products taken part by part without lo x lo: 16 bits; one bf16
-// rounding of the state would leave 2^-9 in every chunk.
+// registers in fp32 (thread: one n, 16 or 8 of the tile's rows).  Operands that
+// the kernels compute are split in bf16 parts and their products taken part by
+// part.  Two parts (18 bits, without lo x lo) do for T, M T, S and X, three
+// (26 bits) are needed for u', which goes into the state as it is; and T's
+// diagonal, b, by far its largest entries, stays out of the product: b X is
+// added in fp32.  The state then is off by 7e-7 in the norm, 5e-6 with two
+// parts throughout, of which T's and u's were nearly all; one bf16 rounding of
+// any of them would leave 1e-3.
 //
 // The decays' exponents are differences of the prefix sums, which are taken
 // in fp64 and kept as two floats: the sums reach hundreds, the differences of
@@ -516,6 +520,7 @@ gdr_tokens_kernel(const GdrParams p, const __grid_constant__ CUtensorMap tm_q, c
 // fp32, so nothing changes) to keep the sums finite.
 constexpr int kGdrC = 64;             // tokens per chunk
 constexpr int kGdrTile = 64;          // state rows per CTA of the scan
+constexpr int kGdrFac = 5 * kGdrC;    // factors of a chunk
 constexpr int kGdrPrepThreads = 256;
 constexpr int kGdrWarps = 16;         // elementwise warps of the scan
 constexpr int kGdrScanThreads = 32 * (kGdrWarps + 2);
@@ -528,7 +533,7 @@ struct GdrChunkParams {
     const float* h_in;            // [B][H][P][N] or null
     __nv_bfloat16* y;             // [B][L][H][P]
     float* h_out;                 // [B][H][P][N]
-    float4* fac;                  // [B][chunks][H][64] per token: X's, u's and y's factor, the chunk's decay
+    float* fac;                   // [B][chunks][H] of 64 tokens' {X's, u's, y's factor, the chunk's decay}, then their b
     int64_t L;
     int H, G, P;
     int chunk0, chunks;           // this launch's chunks of the sequence
@@ -574,6 +579,22 @@ __device__ __forceinline__ bool elect_sync() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
     return p != 0;
 }
+// the same in three parts, `apart` bytes apart
+__device__ __forceinline__ void split3_store8(const float* v, unsigned char* p, int apart) {
+    uint32_t w[3][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 minus = f2(-1.0f, -1.0f);
+        w[0][e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+        float2 r = fma2(f2(bf16_lo(w[0][e]), bf16_hi(w[0][e])), minus, f2(v[2 * e], v[2 * e + 1]));
+        w[1][e] = pack_bf16x2(r.x, r.y);
+        r = fma2(f2(bf16_lo(w[1][e]), bf16_hi(w[1][e])), minus, r);
+        w[2][e] = pack_bf16x2(r.x, r.y);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(p + k * apart) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+}
+
 template <int N>
 struct GdrPrepLayout {
     static constexpr int ld = kGdrC + 4;                          // fp32 rows, 16-byte pieces of 8 rows on different banks
@@ -780,8 +801,10 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                     const int t = lane + 32 * k;
                     const float gam = ex2_fast(cum_hi[t] + cum_lo[t]);
                     const float end = ex2_fast((cum_hi[kGdrC - 1] - cum_hi[t]) + (cum_lo[kGdrC - 1] - cum_lo[t]));
-                    p.fac[unit * kGdrC + t] = make_float4(gam * rk[t], end * rk[t], gam * rq[t],
-                                                          ex2_fast(cum_hi[kGdrC - 1] + cum_lo[kGdrC - 1]));
+                    float* fac = p.fac + unit * kGdrFac;
+                    *reinterpret_cast<float4*>(fac + 4 * t) = make_float4(gam * rk[t], end * rk[t], gam * rq[t],
+                                                                          ex2_fast(cum_hi[kGdrC - 1] + cum_lo[kGdrC - 1]));
+                    fac[4 * kGdrC + t] = bt[t];
                 }
             }
         }
@@ -848,7 +871,7 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         store_tile(Tm + (32 + m) * ld + n, ld, d[0], -1.0f, lane);
     }
     __syncthreads();
-    // T diag(b), split, as rows 0..63 of the operand tile
+    // T (diag(b) included), split, as rows 0..63 of the operand tile
     {
         const int i = tid & (kGdrC - 1), part = tid >> 6;     // a quarter of row i
         float t[16];
@@ -897,6 +920,13 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         }
         fence_proxy_async_smem();
     }
+    if (done && tid < kGdrC) {
+        // M T is taken with all of T; the scan adds b X, T's diagonal, itself
+        const uint32_t off = sw128_off(tid, tid >> 3) + (tid & 7) * 2;
+        *reinterpret_cast<__nv_bfloat16*>(tt + off) = __float2bfloat16_rn(0.0f);
+        *reinterpret_cast<__nv_bfloat16*>(tt + Lay::t_bytes + off) = __float2bfloat16_rn(0.0f);
+        fence_proxy_async_smem();
+    }
     tc_fence_before();
     if (__syncthreads_and(done)) {
         if (tid == 0) {
@@ -926,15 +956,16 @@ struct GdrScanLayout {
     static constexpr int kq_bytes = 2 * kGdrC * N * 2;          // [k; q]
     static constexpr int v_off = kq_bytes;                      // then v [token][64 rows] and the tokens' factors
     static constexpr int fac_off = v_off + kGdrC * 128;
-    static constexpr int in_bytes = fac_off + kGdrC * 16;
+    static constexpr int in_bytes = (fac_off + kGdrFac * 4 + 1023) / 1024 * 1024;
     static constexpr int t_bytes = 2 * kGdrC * 128;             // one part of [T; M T]
     static constexpr int s_bytes = N * 128;                     // one part of S^T [n][64 rows]
-    static constexpr int x_bytes = kGdrC * 128;                 // one part of X or u' [token][64 rows]
+    static constexpr int x_bytes = kGdrC * 128;                 // one part of X or u' [token][64 rows]: two, or three
     static constexpr int stages = 2;
     static constexpr int t_off = stages * in_bytes;
     static constexpr int s_off = t_off + stages * 2 * t_bytes;
-    static constexpr int x_off = s_off + 2 * s_bytes;
-    static constexpr int bar_off = x_off + 2 * x_bytes;
+    // X's and u's first part lies over the end of S, which product 1 has read by then
+    static constexpr int x_off = s_off + 2 * s_bytes - x_bytes;
+    static constexpr int bar_off = x_off + 3 * x_bytes;
     static constexpr int bars = 4 * stages + 6;
     static constexpr int smem_bytes = 1024 + bar_off + bars * 8 + 16;
 };
@@ -957,27 +988,27 @@ __device__ __forceinline__ void tmem_ld8_async(uint32_t taddr, uint32_t (&r)[8])
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }
-// v = the sums of COLS columns at `taddr` and as many 64 further on: a
-// product's two parts
-template <int COLS>
+// v = the sums of COLS columns at `taddr` and as many 64 (and, of three parts,
+// 128) further on: a product's parts
+template <int COLS, int PARTS>
 __device__ __forceinline__ void tmem_ld_sum(uint32_t taddr, float (&v)[COLS]) {
-    uint32_t hi[COLS], lo[COLS];
-    if constexpr (COLS == 16) {
-        tmem_ld16_async(taddr, hi);
-        tmem_ld16_async(taddr + 64, lo);
-    } else {
-        tmem_ld8_async(taddr, hi);
-        tmem_ld8_async(taddr + 64, lo);
+    uint32_t part[PARTS][COLS];
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+        if constexpr (COLS == 16) tmem_ld16_async(taddr + 64 * k, part[k]);
+        else tmem_ld8_async(taddr + 64 * k, part[k]);
     }
     tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < COLS; i += 2) {
-        const float2 r = add2(f2(__uint_as_float(hi[i]), __uint_as_float(hi[i + 1])),
-                              f2(__uint_as_float(lo[i]), __uint_as_float(lo[i + 1])));
+        float2 r = f2(__uint_as_float(part[PARTS - 1][i]), __uint_as_float(part[PARTS - 1][i + 1]));
+#pragma unroll
+        for (int k = PARTS - 2; k >= 0; --k) r = add2(r, f2(__uint_as_float(part[k][i]), __uint_as_float(part[k][i + 1])));
         v[i] = r.x;
         v[i + 1] = r.y;
     }
 }
+
 // 16 elementwise warps, one that issues the products and one that copies.
 // Warp w reaches the tensor-memory lanes of quarter w % 4 and takes columns
 // 16 (w / 4).. of its rows: quarters 0 and 1 hold the tokens' keys (X and u'),
@@ -996,7 +1027,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     using Lay = GdrScanLayout<N>;
     constexpr int kStages = Lay::stages;
     constexpr int kCols = N == 128 ? 16 : 8;             // state entries per thread
-    constexpr uint32_t kD1 = 0, kD2 = 128, kD3 = 256, kTmemCols = 512;    // a product: 64 columns of either part
+    constexpr uint32_t kD1 = 0, kD2 = 128, kD3 = 256, kTmemCols = 512;    // 64 columns of each part
     extern __shared__ __align__(1024) unsigned char gds_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(gds_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + Lay::bar_off);
@@ -1055,13 +1086,13 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 const int tok = (p.chunk0 + first + c) * kGdrC;
                 if (!(ok = mbar_wait_bounded(&kq_free[s], par, p.wait_limit))) break;
                 const int64_t unit = (static_cast<int64_t>(b) * p.chunks + first + c) * p.H + h;
-                mbar_arrive_expect_tx(&kq_full[s], t_rows * N * 2 + (values ? kGdrC * 128 : 0) + kGdrC * 16);
+                mbar_arrive_expect_tx(&kq_full[s], t_rows * N * 2 + (values ? kGdrC * 128 : 0) + kGdrFac * 4);
                 for (int kb = 0; kb < N / 64; ++kb) {
                     tma_load_3d(kq + kb * 16384, &tm_k, g * N + kb * 64, tok, b, &kq_full[s]);
                     if (!STATE) tma_load_3d(kq + kb * 16384 + 8192, &tm_q, g * N + kb * 64, tok, b, &kq_full[s]);
                 }
                 if (values) tma_load_3d(kq + Lay::v_off, &tm_v, h * p.P + tile * kGdrTile, tok, b, &kq_full[s]);
-                bulk_load(kq + Lay::fac_off, p.fac + unit * kGdrC, kGdrC * 16, &kq_full[s]);
+                bulk_load(kq + Lay::fac_off, p.fac + unit * kGdrFac, kGdrFac * 4, &kq_full[s]);
                 ++issued;
                 if (!(ok = mbar_wait_bounded(&t_free[s], par, p.wait_limit))) break;
                 const int row = static_cast<int>(unit * 256);
@@ -1073,12 +1104,12 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
             }
         }
     } else if (warp == kGdrWarps) {
-        // Each product's second operand has its two parts side by side, 128
-        // columns wide: 64 cycles a K step of 16 for both, where two products
+        // Each product's second operand has its parts side by side, 128 columns
+        // wide (u': 192): 64 cycles a K step of 16 for both, where two products
         // of 64 columns take 49 each (bound by the first operand's reads).
         constexpr uint32_t id_12 = umma_idesc_bf16_mn(2 * kGdrC, 2 * kGdrTile, false, true);
         constexpr uint32_t id_lo = umma_idesc_bf16_mn(2 * kGdrC, kGdrTile, false, true);
-        constexpr uint32_t id_3 = umma_idesc_bf16_mn(128, 2 * kGdrTile, true, true);
+        constexpr uint32_t id_3 = umma_idesc_bf16_mn(128, 3 * kGdrTile, true, true);
         const uint32_t sh = smem_addr(sm + Lay::s_off), xh = smem_addr(sm + Lay::x_off);
         for (int c = 0; c < n_chunks; ++c) {
             const int s = c % kStages;
@@ -1163,7 +1194,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         };
         auto add_state = [&](float decay) {
             float add[kCols];
-            tmem_ld_sum<kCols>(lane_base + kD3 + srow0, add);
+            tmem_ld_sum<kCols, 3>(lane_base + kD3 + srow0, add);
 #pragma unroll
             for (int j = 0; j < kCols; j += 2) {
                 const float2 r = fma2(f2(decay, decay), f2(S[j], S[j + 1]), f2(add[j], add[j + 1]));
@@ -1179,6 +1210,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 write_state();
                 if (!wait(&kq_full[s], static_cast<unsigned>((c / kStages) & 1))) break;
                 const float4 f = *reinterpret_cast<const float4*>(in + Lay::fac_off + i * 16);
+                const float bi = *reinterpret_cast<const float*>(in + Lay::fac_off + kGdrC * 16 + i * 4);
                 uint4 v[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
@@ -1186,7 +1218,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 if (!wait(&d_full[0], par)) break;
                 tc_fence_after();
                 float x[16];
-                tmem_ld_sum<16>(lane_base + kD1 + col0, x);
+                tmem_ld_sum<16, 2>(lane_base + kD1 + col0, x);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t off = sw128_off(i, wg * 2 + k);
@@ -1203,17 +1235,18 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 if (!wait(&d_full[1], par)) break;
                 tc_fence_after();
                 float u[16];
-                tmem_ld_sum<16>(lane_base + kD2 + col0, u);
+                tmem_ld_sum<16, 2>(lane_base + kD2 + col0, u);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t off = sw128_off(i, wg * 2 + k);
 #pragma unroll
                     for (int e = 0; e < 8; e += 2) {
-                        const float2 r = mul2(f2(f.y, f.y), f2(u[8 * k + e], u[8 * k + e + 1]));
+                        const float2 r = mul2(f2(f.y, f.y), fma2(f2(bi, bi), f2(x[8 * k + e], x[8 * k + e + 1]),
+                                                                 f2(u[8 * k + e], u[8 * k + e + 1])));
                         u[8 * k + e] = r.x;
                         u[8 * k + e + 1] = r.y;
                     }
-                    split_store8(u + 8 * k, xp + off, xp + Lay::x_bytes + off);
+                    split3_store8(u + 8 * k, xp + off, Lay::x_bytes);
                 }
                 hand_over(&in_full[2]);
                 if (!wait(&d_full[2], par)) break;
@@ -1247,8 +1280,8 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                     if (!wait(&d_full[1], par)) break;
                     tc_fence_after();
                     float d[16], u[16];
-                    tmem_ld_sum<16>(lane_base + kD1 + col0, d);
-                    tmem_ld_sum<16>(lane_base + kD2 + col0, u);
+                    tmem_ld_sum<16, 2>(lane_base + kD1 + col0, d);
+                    tmem_ld_sum<16, 2>(lane_base + kD2 + col0, u);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float2 r = fma2(f2(f.z, f.z), f2(d[2 * e], d[2 * e + 1]), f2(u[2 * e], u[2 * e + 1]));

@@ -2038,7 +2038,7 @@ GdrPlan plan_gdr(int64_t batch, int64_t seqlen, int64_t heads, int64_t headdim, 
     pl.round = std::min(pl.chunks, std::max<int64_t>(1, kGdrRoundUnits / (batch * heads)));
     const int64_t units = batch * heads * pl.round;
     pl.off_fac = kWsHeader;
-    pl.off_t = pl.off_fac + static_cast<size_t>(units) * mm::kGdrC * 16;
+    pl.off_t = pl.off_fac + static_cast<size_t>(units) * mm::kGdrFac * 4;
     pl.off_out = pl.off_t + static_cast<size_t>(units) * 2 * (2 * mm::kGdrC * 128);
     pl.segs = gdr_segments(batch, batch * heads * headdim / mm::kGdrTile, batch * heads * d_state / mm::kGdrTile, pl.round, sms);
     const int64_t rows = batch * heads * (pl.segs - 1) * d_state;
@@ -2087,7 +2087,7 @@ mm_status launch_gdr_chunked(const GdrArgs& a, const GdrPlan& pl, unsigned char*
     p.dt_bias = a.dt_bias;
     p.A = a.A;
     p.y = static_cast<__nv_bfloat16*>(a.y);
-    p.fac = reinterpret_cast<float4*>(w + pl.off_fac);
+    p.fac = reinterpret_cast<float*>(w + pl.off_fac);
     p.seg_out = reinterpret_cast<float*>(w + pl.off_out);
     p.seg_in = reinterpret_cast<float*>(w + pl.off_in);
     p.L = a.seqlen;
