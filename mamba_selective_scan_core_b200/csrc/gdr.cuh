@@ -507,12 +507,12 @@ gdr_tokens_kernel(const GdrParams p, const __grid_constant__ CUtensorMap tm_q, c
 // in one thread's reach: X, u' and y are elementwise.  The state stays in
 // registers in fp32 (thread: one n, 16 or 8 of the tile's rows).  Operands that
 // the kernels compute are split in bf16 parts and their products taken part by
-// part.  Two parts (18 bits, without lo x lo) do for T, M T, S and X, three
-// (26 bits) are needed for u', which goes into the state as it is; and T's
+// part: two (18 bits) for T, M T and S, three (26 bits) for X and u', and T's
 // diagonal, b, by far its largest entries, stays out of the product: b X is
-// added in fp32.  The state then is off by 7e-7 in the norm, 5e-6 with two
-// parts throughout, of which T's and u's were nearly all; one bf16 rounding of
-// any of them would leave 1e-3.
+// added in fp32.  The state then is off by 0.3 to 1e-6 in the norm.  Two parts
+// throughout, the diagonal among them, left 5e-6 and took less time (377
+// us where this takes 465: 16384 tokens x 8 heads); one bf16 rounding of any of
+// them would leave 1e-3.
 //
 // The decays' exponents are differences of the prefix sums, which are taken
 // in fp64 and kept as two floats: the sums reach hundreds, the differences of
@@ -959,7 +959,7 @@ struct GdrScanLayout {
     static constexpr int in_bytes = (fac_off + kGdrFac * 4 + 1023) / 1024 * 1024;
     static constexpr int t_bytes = 2 * kGdrC * 128;             // one part of [T; M T]
     static constexpr int s_bytes = N * 128;                     // one part of S^T [n][64 rows]
-    static constexpr int x_bytes = kGdrC * 128;                 // one part of X or u' [token][64 rows]: two, or three
+    static constexpr int x_bytes = kGdrC * 128;                 // one part of X or u' [token][64 rows], of three
     static constexpr int stages = 2;
     static constexpr int t_off = stages * in_bytes;
     static constexpr int s_off = t_off + stages * 2 * t_bytes;
@@ -1027,7 +1027,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     using Lay = GdrScanLayout<N>;
     constexpr int kStages = Lay::stages;
     constexpr int kCols = N == 128 ? 16 : 8;             // state entries per thread
-    constexpr uint32_t kD1 = 0, kD2 = 128, kD3 = 256, kTmemCols = 512;    // 64 columns of each part
+    constexpr uint32_t kD1 = 0, kD2 = 128, kD3 = 320, kTmemCols = 512;    // 64 columns of each part
     extern __shared__ __align__(1024) unsigned char gds_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(gds_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + Lay::bar_off);
@@ -1105,10 +1105,10 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         }
     } else if (warp == kGdrWarps) {
         // Each product's second operand has its parts side by side, 128 columns
-        // wide (u': 192): 64 cycles a K step of 16 for both, where two products
-        // of 64 columns take 49 each (bound by the first operand's reads).
+        // (S) or 192 (X, u'): 32 cycles a part and K step of 16, where a product
+        // of 64 columns takes 49 (bound by the first operand's reads).
         constexpr uint32_t id_12 = umma_idesc_bf16_mn(2 * kGdrC, 2 * kGdrTile, false, true);
-        constexpr uint32_t id_lo = umma_idesc_bf16_mn(2 * kGdrC, kGdrTile, false, true);
+        constexpr uint32_t id_x = umma_idesc_bf16_mn(2 * kGdrC, 3 * kGdrTile, false, true);
         constexpr uint32_t id_3 = umma_idesc_bf16_mn(128, 3 * kGdrTile, true, true);
         const uint32_t sh = smem_addr(sm + Lay::s_off), xh = smem_addr(sm + Lay::x_off);
         for (int c = 0; c < n_chunks; ++c) {
@@ -1132,8 +1132,8 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
 #pragma unroll
                 for (int kk = 0; kk < kGdrC / 16; ++kk) {
                     umma_bf16(tmem + kD2, umma_desc_sw128(th + kk * 32), umma_desc_sw128_mn(xh + kk * 2048, Lay::x_bytes),
-                              id_12, kk > 0 ? 1u : 0u);
-                    umma_bf16(tmem + kD2, umma_desc_sw128(tl + kk * 32), umma_desc_sw128_mn(xh + kk * 2048, 0), id_lo, 1u);
+                              id_x, kk > 0 ? 1u : 0u);
+                    umma_bf16(tmem + kD2, umma_desc_sw128(tl + kk * 32), umma_desc_sw128_mn(xh + kk * 2048, Lay::x_bytes), id_12, 1u);
                 }
                 umma_commit(&d_full[1]);
                 umma_commit(&t_free[s]);
@@ -1229,13 +1229,13 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                         x[8 * k + 2 * e] = r.x;
                         x[8 * k + 2 * e + 1] = r.y;
                     }
-                    split_store8(x + 8 * k, xp + off, xp + Lay::x_bytes + off);
+                    split3_store8(x + 8 * k, xp + off, Lay::x_bytes);
                 }
                 hand_over(&in_full[1]);
                 if (!wait(&d_full[1], par)) break;
                 tc_fence_after();
                 float u[16];
-                tmem_ld_sum<16, 2>(lane_base + kD2 + col0, u);
+                tmem_ld_sum<16, 3>(lane_base + kD2 + col0, u);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t off = sw128_off(i, wg * 2 + k);
@@ -1281,7 +1281,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                     tc_fence_after();
                     float d[16], u[16];
                     tmem_ld_sum<16, 2>(lane_base + kD1 + col0, d);
-                    tmem_ld_sum<16, 2>(lane_base + kD2 + col0, u);
+                    tmem_ld_sum<16, 3>(lane_base + kD2 + col0, u);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float2 r = fma2(f2(f.z, f.z), f2(d[2 * e], d[2 * e + 1]), f2(u[2 * e], u[2 * e + 1]));
