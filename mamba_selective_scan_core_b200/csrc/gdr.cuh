@@ -510,9 +510,19 @@ gdr_tokens_kernel(const GdrParams p, const __grid_constant__ CUtensorMap tm_q, c
 // part: two (18 bits) for T, M T and S, three (26 bits) for X and u', and T's
 // diagonal, b, by far its largest entries, stays out of the product: b X is
 // added in fp32.  The state then is off by 0.3 to 1e-6 in the norm.  Two parts
-// throughout, the diagonal among them, left 5e-6 and took less time (377
-// us where this takes 465: 16384 tokens x 8 heads); one bf16 rounding of any of
+// throughout, the diagonal among them, left 5e-6 and took less time (377 us
+// where this takes 465: 16384 tokens x 8 heads); one bf16 rounding of any of
 // them would leave 1e-3.
+//
+// What bounds them.  The prep kernel: the phases of a chunk's system, most of
+// which keep two to four of its eight warps busy (warps wait at barriers 40% of
+// their time; 0.46 instructions a cycle and scheduler): 24 ns a chunk of a head
+// with four blocks an SM, 10 us for one alone.  The scan: its chain of three
+// products a chunk, 2.9 us of which about 1300 cycles are the products', 1500
+// the elementwise work on two of the four schedulers (tensor-memory lanes
+// 0..63, the keys' rows, belong to those), the rest waits and hand-overs; the
+// tensor pipe is busy 26% of the time.  Longer chunks need more shared memory
+// than there is for [T; M T].
 //
 // The decays' exponents are differences of the prefix sums, which are taken
 // in fp64 and kept as two floats: the sums reach hundreds, the differences of

@@ -24,6 +24,12 @@
 // to fewer bits before the output.  The zero point's part is
 // s (8 - z) sum_k x[m, k], whose sum is one more mma with a matrix of ones.
 //
+// What bounds it: the integer pipe.  A product's 16 x 128 weights take 32
+// mask-and-ors, 24 shifts and 16 byte permutes there, at two cycles each; in
+// 16384 x 16384 with one row, 52 us, the copies alone take 29 us, the rest alone
+// 47 (38 without the shifts, 44 without the subtractions or the permutes).
+// 16384 x 4096, one row: 15.2 us, 2.3 TB/s.
+//
 // Unpacking: (w >> 4i) & 0x000f000f | 0x43004300 is the bf16 pair
 // (128 + c_i, 128 + c_{i+4}) of a word of eight; one packed subtraction of 136
 // leaves c - 8.  The pairs (i, i + 4) fix the order of the inputs within a
