@@ -518,7 +518,7 @@ gdr_tokens_kernel(const GdrParams p, const __grid_constant__ CUtensorMap tm_q, c
 // which keep two to four of its eight warps busy (warps wait at barriers 40% of
 // their time; 0.46 instructions a cycle and scheduler): 24 ns a chunk of a head
 // with four blocks an SM, 10 us for one alone.  The scan: its chain of three
-// products a chunk, 2.9 us of which about 1300 cycles are the products', 1500
+// products a chunk, 3.1 us, of which about 1500 cycles are the products', 2000
 // the elementwise work on two of the four schedulers (tensor-memory lanes
 // 0..63, the keys' rows, belong to those), the rest waits and hand-overs; the
 // tensor pipe is busy 26% of the time.  Longer chunks need more shared memory

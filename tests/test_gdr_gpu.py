@@ -144,10 +144,12 @@ def test_long_sequences_of_few_heads(B, L, G, H, P, N, dt_mean):
     check(gdr_inputs(B, L, G, H, P, N, seed=L, dt_mean=dt_mean, h0=B == 1))
 
 
-def test_more_chunks_than_one_round():
-    """A batch whose chunks' workspace is kept for part of the sequence at a
-    time: as two calls, the second from the first one's state."""
-    B, L, H, P, N, cut = 8, 64 * 130 + 5, 16, 64, 64, 4096
+@pytest.mark.parametrize("B,L,H,cut", [(8, 64 * 130 + 5, 16, 4096), (1, 64 * 8192 + 1000, 2, 300000)])
+def test_more_chunks_than_one_round(B, L, H, cut):
+    """Chunks whose workspace is kept for part of the sequence at a time, of
+    many heads and (in segments) of few: as two calls, the second from the
+    first one's state."""
+    P, N = 64, 64
     g = torch.Generator(device="cuda").manual_seed(97)
 
     def normal(*shape):
