@@ -509,7 +509,7 @@ gdr_tokens_kernel(const GdrParams p, const __grid_constant__ CUtensorMap tm_q, c
 // the kernels compute are split in bf16 parts and their products taken part by
 // part: two (18 bits) for T, M T and S, three (26 bits) for X and u', and T's
 // diagonal, b, by far its largest entries, stays out of the product: b X is
-// added in fp32.  The state then is off by 0.3 to 1e-6 in the norm.  Two parts
+// added in fp32.  The state then is off by 0.3 to 1.2e-6 in the norm.  Two parts
 // throughout, the diagonal among them, left 5e-6 and took less time (377 us
 // where this takes 465: 16384 tokens x 8 heads); one bf16 rounding of any of
 // them would leave 1e-3.
