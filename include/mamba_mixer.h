@@ -622,8 +622,8 @@ mm_status mamba_m3_state_update(const void* x, const void* z, const void* dt, co
  * lengths run as one batch that way (the padding's y is still written).
  *
  * bf16 calls of more than some tens of tokens run in chunks of 64 as dense
- * products on the tensor cores, what they compute of their operands in two or
- * three bf16 parts (18 or 26 bits), sums and the state in fp32; long ones of few
+ * products on the tensor cores, what they compute of their operands in three
+ * bf16 parts (26 bits), sums and the state in fp32; long ones of few
  * heads in segments of chunks at once.  Other calls run token by token in fp32.
  * Which one is a function of the sizes, the type and the SM count alone.
  *

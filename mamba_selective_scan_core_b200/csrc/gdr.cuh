@@ -506,13 +506,16 @@ gdr_tokens_kernel(const GdrParams p, const __grid_constant__ CUtensorMap tm_q, c
 // product of their own, and the value of a row of [k; q] S^T or [T; M T] X is
 // in one thread's reach: X, u' and y are elementwise.  The state stays in
 // registers in fp32 (thread: one n, 16 or 8 of the tile's rows).  Operands that
-// the kernels compute are split in bf16 parts and their products taken part by
-// part: two (18 bits) for T, M T and S, three (26 bits) for X and u', and T's
-// diagonal, b, by far its largest entries, stays out of the product: b X is
-// added in fp32.  The state then is off by 0.3 to 1.2e-6 in the norm.  Two parts
-// throughout, the diagonal among them, left 5e-6 and took less time (377 us
-// where this takes 465: 16384 tokens x 8 heads); one bf16 rounding of any of
-// them would leave 1e-3.
+// the kernels compute (S, T, M, M T, X and u') are the sums of three bf16 parts
+// (26 bits), their products taken part by part, so a chunk is as exact as fp32
+// sums are: the state after a prefill is off by 1.0 to 1.7e-7 in the norm where
+// the same formulas in fp32 are off by 0.9 to 1.6e-7, and y's error before it is
+// rounded is as small.  T's diagonal, b, by far its largest entries, stays out
+// of the product: b X is added in fp32.  Two parts of S, T, M and M T took 301
+// us where this takes 344 (4096 tokens x 64 heads, N = 128) and left 3 to 9e-7
+// of the state and 4e-6 of y before its rounding; two parts throughout, the
+// diagonal among them, 5e-6 of the state; one bf16 rounding of any of them
+// would leave 1e-3.
 //
 // What bounds them.  The prep kernel: the phases of a chunk's system, most of
 // which keep two to four of its eight warps busy (warps wait at barriers 40% of
@@ -531,6 +534,7 @@ gdr_tokens_kernel(const GdrParams p, const __grid_constant__ CUtensorMap tm_q, c
 constexpr int kGdrC = 64;             // tokens per chunk
 constexpr int kGdrTile = 64;          // state rows per CTA of the scan
 constexpr int kGdrFac = 5 * kGdrC;    // factors of a chunk
+constexpr int kGdrSolved = 6 * kGdrC; // rows of 64 bf16 of its solved system: [T; M T] in three parts
 constexpr int kGdrPrepThreads = 256;
 constexpr int kGdrWarps = 16;         // elementwise warps of the scan
 constexpr int kGdrScanThreads = 32 * (kGdrWarps + 2);
@@ -563,23 +567,6 @@ __device__ __forceinline__ void gdr_fail(const GdrChunkParams& p) {
 
 // two floats at a time (add, multiply and fma take a pair per instruction)
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
-// (v.x, v.y) = hi + lo as split_bf16x2
-__device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
-    hi = pack_bf16x2(v.x, v.y);
-    const float2 r = fma2(f2(bf16_lo(hi), bf16_hi(hi)), f2(-1.0f, -1.0f), v);
-    lo = pack_bf16x2(r.x, r.y);
-}
-// v[8] -> one 16-byte piece of each part
-__device__ __forceinline__ void split_store8(const float* v, unsigned char* hi_p, unsigned char* lo_p) {
-    uint4 hi, lo;
-    split2(f2(v[0], v[1]), hi.x, lo.x);
-    split2(f2(v[2], v[3]), hi.y, lo.y);
-    split2(f2(v[4], v[5]), hi.z, lo.z);
-    split2(f2(v[6], v[7]), hi.w, lo.w);
-    *reinterpret_cast<uint4*>(hi_p) = hi;
-    *reinterpret_cast<uint4*>(lo_p) = lo;
-}
-
 // true in one lane of a converged warp, in a form that keeps the other
 // operands of what it guards in uniform registers (a tcgen05.mma takes those:
 // 32 to 64 cycles apart then, 46 and more when each operand is moved there
@@ -589,8 +576,9 @@ __device__ __forceinline__ bool elect_sync() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
     return p != 0;
 }
-// the same in three parts, `apart` bytes apart
-__device__ __forceinline__ void split3_store8(const float* v, unsigned char* p, int apart) {
+// v[8] = the sum of three bf16 parts (8 bits each, round to nearest): a 16-byte
+// piece of each
+__device__ __forceinline__ void split3(const float* v, uint4 (&part)[3]) {
     uint32_t w[3][4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -602,24 +590,34 @@ __device__ __forceinline__ void split3_store8(const float* v, unsigned char* p, 
         w[2][e] = pack_bf16x2(r.x, r.y);
     }
 #pragma unroll
-    for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(p + k * apart) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+    for (int k = 0; k < 3; ++k) part[k] = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+}
+// the parts `apart` bytes apart
+__device__ __forceinline__ void split3_store8(const float* v, unsigned char* p, int apart) {
+    uint4 part[3];
+    split3(v, part);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(p + k * apart) = part[k];
 }
 
 template <int N>
 struct GdrPrepLayout {
     static constexpr int ld = kGdrC + 4;                          // fp32 rows, 16-byte pieces of 8 rows on different banks
     static constexpr int kq_bytes = 2 * kGdrC * N * 2;            // [k; q]: a [128][64] block per 64 of N
-    static constexpr int t_bytes = 2 * kGdrC * 128;               // [T; M T], one part
+    static constexpr int part = kGdrC * 128;                      // one part of T, of M or of M T
     static constexpr int mat_bytes = kGdrC * ld * 4;
-    // L and its inverse (fp32) lie over k and q once [k; q] k^T is taken, the
-    // rows [T; M T] over those once T is read
+    // L and its inverse (fp32) lie over k and q once [k; q] k^T is taken, T's
+    // three parts and M's third over those once T is read; M T's parts take the
+    // place of M's
     static constexpr int l_off = 0;
     static constexpr int inv_off = mat_bytes;
-    static constexpr int big = 2 * mat_bytes;
     static constexpr int kq_off = 0, t_off = 0;
-    static constexpr int m_off = (big + 1023) / 1024 * 1024;
-    static_assert(m_off >= kq_bytes && m_off >= 2 * t_bytes, "k and q, and the operand rows, fit below M");
-    static constexpr int f_off = m_off + 2 * kGdrC * 128;
+    static constexpr int m3_off = 3 * part;
+    static constexpr int m_off = (2 * mat_bytes + 1023) / 1024 * 1024;
+    static_assert(m_off >= kq_bytes && m_off >= m3_off + part, "k and q, T's parts and M's third fit below M");
+    // where M's part k lies
+    __device__ static constexpr int m_part(int k) { return k < 2 ? m_off + k * part : m3_off; }
+    static constexpr int f_off = m_off + 2 * part;
     static constexpr int floats = 5 * kGdrC;
     static constexpr int bar_off = f_off + floats * 4 + 32;
     static constexpr int smem_bytes = 1024 + bar_off + 3 * 8 + 16;
@@ -686,8 +684,7 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     unsigned char* kq = sm + Lay::kq_off;
     float* Lm = reinterpret_cast<float*>(sm + Lay::l_off);
     float* Tm = reinterpret_cast<float*>(sm + Lay::inv_off);
-    unsigned char* mt = sm + Lay::m_off;                 // M hi, lo: 64 rows each
-    unsigned char* tt = sm + Lay::t_off;                 // [T; M T] hi, lo: 128 rows each
+    unsigned char* tt = sm + Lay::t_off;                 // T's parts, 64 rows each
     float* cum_hi = reinterpret_cast<float*>(sm + Lay::f_off);   // prefix sums times log2(e), hi + lo
     float* cum_lo = cum_hi + kGdrC;
     float* bt = cum_lo + kGdrC;                          // b_t
@@ -780,7 +777,9 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     const bool ready = __syncthreads_and(ok);
 
     // row i of L (quarters 0, 1) or of M, 32 columns; the columns past the
-    // row's own 32-column block are zero
+    // row's own 32-column block are zero.  M's third part waits in registers
+    // until its place is free.
+    uint4 m3[4] = {};
     if (ready) {
         const int i = (q & 1) * 32 + lane;
         const bool key = q < 2;
@@ -826,7 +825,11 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint32_t off = sw128_off(i, half * 4 + e);
-                split_store8(m + 8 * e, mt + off, mt + 8192 + off);
+                uint4 part[3];
+                split3(m + 8 * e, part);
+                *reinterpret_cast<uint4*>(sm + Lay::m_part(0) + off) = part[0];
+                *reinterpret_cast<uint4*>(sm + Lay::m_part(1) + off) = part[1];
+                m3[e] = part[2];
             }
         }
     }
@@ -881,7 +884,7 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         store_tile(Tm + (32 + m) * ld + n, ld, d[0], -1.0f, lane);
     }
     __syncthreads();
-    // T (diag(b) included), split, as rows 0..63 of the operand tile
+    // T (diag(b) included) in its parts
     {
         const int i = tid & (kGdrC - 1), part = tid >> 6;     // a quarter of row i
         float t[16];
@@ -898,9 +901,13 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const uint32_t off = sw128_off(i, part * 2 + e);
-            split_store8(t + 8 * e, tt + off, tt + Lay::t_bytes + off);
+            split3_store8(t + 8 * e, tt + off, Lay::part);
         }
     }
+    if (q >= 2)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(sm + Lay::m_part(2) + sw128_off((q & 1) * 32 + lane, half * 4 + e)) = m3[e];
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -909,13 +916,14 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     // precedes the tile, and their results are not read); B = T [l][j], MN-major
     if (ready && warp == 7 && elect_sync()) {
         constexpr uint32_t idesc = umma_idesc_bf16_mn(2 * kGdrC, kGdrC, false, true);
-        const uint32_t mh = smem_addr(mt) - 8192, ml = smem_addr(mt), th = smem_addr(tt), tl = th + Lay::t_bytes;
 #pragma unroll
-        for (int kk = 0; kk < kGdrC / 16; ++kk) {
-            umma_bf16(tmem, umma_desc_sw128(mh + kk * 32), umma_desc_sw128_mn(th + kk * 2048, 0), idesc, kk > 0 ? 1u : 0u);
-            umma_bf16(tmem, umma_desc_sw128(mh + kk * 32), umma_desc_sw128_mn(tl + kk * 2048, 0), idesc, 1u);
-            umma_bf16(tmem, umma_desc_sw128(ml + kk * 32), umma_desc_sw128_mn(th + kk * 2048, 0), idesc, 1u);
-        }
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+            for (int j = 0; i + j < 3; ++j)
+#pragma unroll
+                for (int kk = 0; kk < kGdrC / 16; ++kk)
+                    umma_bf16(tmem, umma_desc_sw128(smem_addr(sm) + Lay::m_part(i) - Lay::part + kk * 32),
+                              umma_desc_sw128_mn(smem_addr(tt) + j * Lay::part + kk * 2048, 0), idesc, i + j + kk > 0 ? 1u : 0u);
         umma_commit(&bars[2]);
     }
     const bool done = ready && warp_wait(&bars[2], 0, p.wait_limit);
@@ -925,23 +933,30 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         tmem_ld32(lane_base + half * 32, m);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t off = sw128_off(q * 32 + lane, half * 4 + e);
-            split_store8(m + 8 * e, tt + off, tt + Lay::t_bytes + off);
+            const uint32_t off = sw128_off((q & 1) * 32 + lane, half * 4 + e);
+            uint4 part[3];
+            split3(m + 8 * e, part);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(sm + Lay::m_part(k) + off) = part[k];
         }
         fence_proxy_async_smem();
     }
     if (done && tid < kGdrC) {
         // M T is taken with all of T; the scan adds b X, T's diagonal, itself
         const uint32_t off = sw128_off(tid, tid >> 3) + (tid & 7) * 2;
-        *reinterpret_cast<__nv_bfloat16*>(tt + off) = __float2bfloat16_rn(0.0f);
-        *reinterpret_cast<__nv_bfloat16*>(tt + Lay::t_bytes + off) = __float2bfloat16_rn(0.0f);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<__nv_bfloat16*>(tt + k * Lay::part + off) = __float2bfloat16_rn(0.0f);
         fence_proxy_async_smem();
     }
     tc_fence_before();
     if (__syncthreads_and(done)) {
         if (tid == 0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) tma_store_2d(&tm_t, tt + k * 8192, 0, static_cast<int>(unit * 256 + k * 64));
+            for (int k = 0; k < 3; ++k) {
+                const int row = static_cast<int>(unit * kGdrSolved + k * 2 * kGdrC);
+                tma_store_2d(&tm_t, tt + k * Lay::part, 0, row);
+                tma_store_2d(&tm_t, sm + Lay::m_part(k), 0, row + kGdrC);
+            }
             bulk_commit_group();
             bulk_wait_read_all();
         }
@@ -967,16 +982,17 @@ struct GdrScanLayout {
     static constexpr int v_off = kq_bytes;                      // then v [token][64 rows] and the tokens' factors
     static constexpr int fac_off = v_off + kGdrC * 128;
     static constexpr int in_bytes = (fac_off + kGdrFac * 4 + 1023) / 1024 * 1024;
-    static constexpr int t_bytes = 2 * kGdrC * 128;             // one part of [T; M T]
-    static constexpr int s_bytes = N * 128;                     // one part of S^T [n][64 rows]
+    static constexpr int t_bytes = 2 * kGdrC * 128;             // one part of [T; M T], of three
+    static constexpr int s_bytes = N * 128;                     // one part of S^T [n][64 rows], of three
     static constexpr int x_bytes = kGdrC * 128;                 // one part of X or u' [token][64 rows], of three
-    static constexpr int stages = 2;
+    static constexpr int stages = 2;                            // of the inputs; the solved rows have one place
     static constexpr int t_off = stages * in_bytes;
-    static constexpr int s_off = t_off + stages * 2 * t_bytes;
-    // X's and u's first part lies over the end of S, which product 1 has read by then
-    static constexpr int x_off = s_off + 2 * s_bytes - x_bytes;
-    static constexpr int bar_off = x_off + 3 * x_bytes;
-    static constexpr int bars = 4 * stages + 6;
+    static constexpr int s_off = t_off + 3 * t_bytes;
+    // X and u' lie over S, which product 1 has read by then
+    static constexpr int x_off = s_off;
+    static_assert(x_bytes <= s_bytes, "X's parts fit S's place");
+    static constexpr int bar_off = s_off + 3 * s_bytes;
+    static constexpr int bars = 2 * stages + 8;
     static constexpr int smem_bytes = 1024 + bar_off + bars * 8 + 16;
 };
 
@@ -1037,14 +1053,14 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     using Lay = GdrScanLayout<N>;
     constexpr int kStages = Lay::stages;
     constexpr int kCols = N == 128 ? 16 : 8;             // state entries per thread
-    constexpr uint32_t kD1 = 0, kD2 = 128, kD3 = 320, kTmemCols = 512;    // 64 columns of each part
+    constexpr uint32_t kD1 = 0, kD2 = 192, kD3 = 384, kTmemCols = 512;    // 64 columns of each part
     extern __shared__ __align__(1024) unsigned char gds_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(gds_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* kq_full = reinterpret_cast<uint64_t*>(sm + Lay::bar_off);
     uint64_t* kq_free = kq_full + kStages;
     uint64_t* t_full = kq_free + kStages;
-    uint64_t* t_free = t_full + kStages;
-    uint64_t* d_full = t_free + kStages;                 // [3] products 1, 2, 3
+    uint64_t* t_free = t_full + 1;
+    uint64_t* d_full = t_free + 1;                       // [3] products 1, 2, 3
     uint64_t* in_full = d_full + 3;                      // [3] S, X, u' written
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + 3);
 
@@ -1062,9 +1078,9 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&kq_full[s], 1);
             mbar_init(&kq_free[s], 1);
-            mbar_init(&t_full[s], 1);
-            mbar_init(&t_free[s], 1);
         }
+        mbar_init(t_full, 1);
+        mbar_init(t_free, 1);
         for (int i = 0; i < 3; ++i) mbar_init(&d_full[i], 1);
         mbar_init(&in_full[0], kGdrWarps);
         mbar_init(&in_full[1], kGdrWarps / 2);
@@ -1092,7 +1108,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 const int s = c % kStages;
                 const unsigned par = static_cast<unsigned>(((c / kStages) & 1) ^ 1);
                 unsigned char* kq = sm + s * Lay::in_bytes;
-                unsigned char* tt = sm + Lay::t_off + s * 2 * Lay::t_bytes;
+                unsigned char* tt = sm + Lay::t_off;
                 const int tok = (p.chunk0 + first + c) * kGdrC;
                 if (!(ok = mbar_wait_bounded(&kq_free[s], par, p.wait_limit))) break;
                 const int64_t unit = (static_cast<int64_t>(b) * p.chunks + first + c) * p.H + h;
@@ -1104,58 +1120,67 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 if (values) tma_load_3d(kq + Lay::v_off, &tm_v, h * p.P + tile * kGdrTile, tok, b, &kq_full[s]);
                 bulk_load(kq + Lay::fac_off, p.fac + unit * kGdrFac, kGdrFac * 4, &kq_full[s]);
                 ++issued;
-                if (!(ok = mbar_wait_bounded(&t_free[s], par, p.wait_limit))) break;
-                const int row = static_cast<int>(unit * 256);
-                mbar_arrive_expect_tx(&t_full[s], 2 * t_rows * 128);
+                if (!(ok = mbar_wait_bounded(t_free, static_cast<unsigned>(c & 1) ^ 1u, p.wait_limit))) break;
+                const int row = static_cast<int>(unit * kGdrSolved);
+                mbar_arrive_expect_tx(t_full, 3 * t_rows * 128);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (!STATE || k % 2 == 0) tma_load_2d(tt + k * 8192, &tm_t, 0, row + k * 64, &t_full[s]);
+                for (int k = 0; k < 6; ++k)
+                    if (!STATE || k % 2 == 0) tma_load_2d(tt + k * 8192, &tm_t, 0, row + k * 64, t_full);
                 ++issued;
             }
         }
     } else if (warp == kGdrWarps) {
-        // Each product's second operand has its parts side by side, 128 columns
-        // (S) or 192 (X, u'): 32 cycles a part and K step of 16, where a product
-        // of 64 columns takes 49 (bound by the first operand's reads).
-        constexpr uint32_t id_12 = umma_idesc_bf16_mn(2 * kGdrC, 2 * kGdrTile, false, true);
-        constexpr uint32_t id_x = umma_idesc_bf16_mn(2 * kGdrC, 3 * kGdrTile, false, true);
-        constexpr uint32_t id_3 = umma_idesc_bf16_mn(128, 3 * kGdrTile, true, true);
-        const uint32_t sh = smem_addr(sm + Lay::s_off), xh = smem_addr(sm + Lay::x_off);
+        // A product's second operand has its parts side by side, 192 columns: 32
+        // cycles a part and K step of 16, where a product of 64 columns takes 49
+        // (bound by the first operand's reads).  Of two operands in parts, the
+        // products whose parts' places add up to more than the third's are left
+        // out (2^-26).  u's third part goes onto its second one's columns:
+        // tensor memory holds 8 parts, not 9.
+        constexpr uint32_t id_3 = umma_idesc_bf16_mn(2 * kGdrC, 3 * kGdrTile, false, true);
+        constexpr uint32_t id_2 = umma_idesc_bf16_mn(2 * kGdrC, 2 * kGdrTile, false, true);
+        constexpr uint32_t id_1 = umma_idesc_bf16_mn(2 * kGdrC, kGdrTile, false, true);
+        constexpr uint32_t id_u2 = umma_idesc_bf16_mn(128, 2 * kGdrTile, true, true);
+        constexpr uint32_t id_u1 = umma_idesc_bf16_mn(128, kGdrTile, true, true);
+        const uint32_t sh = smem_addr(sm + Lay::s_off), xh = smem_addr(sm + Lay::x_off), th = smem_addr(sm + Lay::t_off);
         for (int c = 0; c < n_chunks; ++c) {
             const int s = c % kStages;
             const unsigned par = static_cast<unsigned>(c & 1), spar = static_cast<unsigned>((c / kStages) & 1);
             const uint32_t kq = smem_addr(sm + s * Lay::in_bytes);
-            const uint32_t th = smem_addr(sm + Lay::t_off + s * 2 * Lay::t_bytes), tl = th + Lay::t_bytes;
             if (!(ok = warp_wait(&kq_full[s], spar, p.wait_limit) && warp_wait(&in_full[0], par, p.wait_limit))) break;
             tc_fence_after();
             if (elect_sync()) {
 #pragma unroll
                 for (int kk = 0; kk < N / 16; ++kk)
                     umma_bf16(tmem + kD1, umma_desc_sw128(kq + (kk >> 2) * 16384 + (kk & 3) * 32),
-                              umma_desc_sw128_mn(sh + kk * 2048, Lay::s_bytes), id_12, kk > 0 ? 1u : 0u);
+                              umma_desc_sw128_mn(sh + kk * 2048, Lay::s_bytes), id_3, kk > 0 ? 1u : 0u);
                 umma_commit(&d_full[0]);
             }
             ++issued;
-            if (!(ok = warp_wait(&t_full[s], spar, p.wait_limit) && warp_wait(&in_full[1], par, p.wait_limit))) break;
+            if (!(ok = warp_wait(t_full, par, p.wait_limit) && warp_wait(&in_full[1], par, p.wait_limit))) break;
             tc_fence_after();
             if (elect_sync()) {
 #pragma unroll
                 for (int kk = 0; kk < kGdrC / 16; ++kk) {
-                    umma_bf16(tmem + kD2, umma_desc_sw128(th + kk * 32), umma_desc_sw128_mn(xh + kk * 2048, Lay::x_bytes),
-                              id_x, kk > 0 ? 1u : 0u);
-                    umma_bf16(tmem + kD2, umma_desc_sw128(tl + kk * 32), umma_desc_sw128_mn(xh + kk * 2048, Lay::x_bytes), id_12, 1u);
+                    umma_bf16(tmem + kD2, umma_desc_sw128(th + kk * 32), umma_desc_sw128_mn(xh + kk * 2048, Lay::x_bytes), id_3,
+                              kk > 0 ? 1u : 0u);
+                    umma_bf16(tmem + kD2, umma_desc_sw128(th + Lay::t_bytes + kk * 32),
+                              umma_desc_sw128_mn(xh + kk * 2048, Lay::x_bytes), id_2, 1u);
+                    umma_bf16(tmem + kD2, umma_desc_sw128(th + 2 * Lay::t_bytes + kk * 32), umma_desc_sw128_mn(xh + kk * 2048, 0),
+                              id_1, 1u);
                 }
                 umma_commit(&d_full[1]);
-                umma_commit(&t_free[s]);
+                umma_commit(t_free);
             }
             ++issued;
             if (!(ok = warp_wait(&in_full[2], par, p.wait_limit))) break;
             tc_fence_after();
             if (elect_sync()) {
 #pragma unroll
-                for (int kk = 0; kk < kGdrC / 16; ++kk)
-                    umma_bf16(tmem + kD3, umma_desc_sw128_mn(kq + kk * 2048, N == 128 ? 16384 : 0),
-                              umma_desc_sw128_mn(xh + kk * 2048, Lay::x_bytes), id_3, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < kGdrC / 16; ++kk) {
+                    const uint64_t kt = umma_desc_sw128_mn(kq + kk * 2048, N == 128 ? 16384 : 0);
+                    umma_bf16(tmem + kD3, kt, umma_desc_sw128_mn(xh + kk * 2048, Lay::x_bytes), id_u2, kk > 0 ? 1u : 0u);
+                    umma_bf16(tmem + kD3 + 64, kt, umma_desc_sw128_mn(xh + 2 * Lay::x_bytes + kk * 2048, 0), id_u1, 1u);
+                }
                 umma_commit(&d_full[2]);
                 umma_commit(&kq_free[s]);
             }
@@ -1198,13 +1223,13 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
 #pragma unroll
             for (int k = 0; k < kCols / 8; ++k) {
                 const uint32_t off = sw128_off(n, srow0 / 8 + k);
-                split_store8(S + 8 * k, sp + off, sp + Lay::s_bytes + off);
+                split3_store8(S + 8 * k, sp + off, Lay::s_bytes);
             }
             hand_over(&in_full[0]);
         };
         auto add_state = [&](float decay) {
             float add[kCols];
-            tmem_ld_sum<kCols, 3>(lane_base + kD3 + srow0, add);
+            tmem_ld_sum<kCols, 2>(lane_base + kD3 + srow0, add);
 #pragma unroll
             for (int j = 0; j < kCols; j += 2) {
                 const float2 r = fma2(f2(decay, decay), f2(S[j], S[j + 1]), f2(add[j], add[j + 1]));
@@ -1228,7 +1253,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 if (!wait(&d_full[0], par)) break;
                 tc_fence_after();
                 float x[16];
-                tmem_ld_sum<16, 2>(lane_base + kD1 + col0, x);
+                tmem_ld_sum<16, 3>(lane_base + kD1 + col0, x);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t off = sw128_off(i, wg * 2 + k);
@@ -1290,7 +1315,7 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                     if (!wait(&d_full[1], par)) break;
                     tc_fence_after();
                     float d[16], u[16];
-                    tmem_ld_sum<16, 2>(lane_base + kD1 + col0, d);
+                    tmem_ld_sum<16, 3>(lane_base + kD1 + col0, d);
                     tmem_ld_sum<16, 3>(lane_base + kD2 + col0, u);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -1317,7 +1342,8 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         if (warp == kGdrWarps + 1 && elect_one_lane()) {
             for (int k = max(0, issued - 2 * kStages); k < issued; ++k) {
                 const int c = k / 2, s = c % kStages;
-                mbar_wait_bounded(k % 2 ? &t_full[s] : &kq_full[s], static_cast<unsigned>((c / kStages) & 1), 1u << 20);
+                if (k % 2) mbar_wait_bounded(t_full, static_cast<unsigned>(c & 1), 1u << 20);
+                else mbar_wait_bounded(&kq_full[s], static_cast<unsigned>((c / kStages) & 1), 1u << 20);
             }
         } else if (warp == kGdrWarps && elect_one_lane() && issued > 0) {
             const int k = issued - 1;

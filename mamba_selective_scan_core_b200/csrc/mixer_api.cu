@@ -2002,7 +2002,7 @@ mm_status launch_gdr_recurrent(const mm::GdrParams& p, const GdrArgs& a, cudaStr
 // reads one while its last writes the other).
 constexpr int64_t kGdrManyRows = 16384;        // state rows of all heads
 int64_t gdr_chunked_min(int64_t rows) { return rows >= kGdrManyRows ? 16 : 44; }
-constexpr int64_t kGdrRoundUnits = 16384;      // 33 KB each
+constexpr int64_t kGdrRoundUnits = 16384;      // 50 KB each
 struct GdrPlan {
     bool chunked = false;
     int64_t chunks = 0, round = 0;             // of a sequence; of a launch
@@ -2039,7 +2039,7 @@ GdrPlan plan_gdr(int64_t batch, int64_t seqlen, int64_t heads, int64_t headdim, 
     const int64_t units = batch * heads * pl.round;
     pl.off_fac = kWsHeader;
     pl.off_t = pl.off_fac + static_cast<size_t>(units) * mm::kGdrFac * 4;
-    pl.off_out = pl.off_t + static_cast<size_t>(units) * 2 * (2 * mm::kGdrC * 128);
+    pl.off_out = pl.off_t + static_cast<size_t>(units) * mm::kGdrSolved * 128;
     pl.segs = gdr_segments(batch, batch * heads * headdim / mm::kGdrTile, batch * heads * d_state / mm::kGdrTile, pl.round, sms);
     const int64_t rows = batch * heads * (pl.segs - 1) * d_state;
     pl.off_in = pl.off_out + static_cast<size_t>(rows * (headdim + d_state)) * 4;
@@ -2074,7 +2074,7 @@ mm_status launch_gdr_chunked(const GdrArgs& a, const GdrPlan& pl, unsigned char*
     };
     if (!tile_map(&tq, a.q, a.groups * N, a.q_stride) || !tile_map(&tk, a.k, a.groups * N, a.k_stride) ||
         !tile_map(&tv, a.v, a.heads * a.headdim, a.v_stride) ||
-        !encode_gemm_2d(&tt, w + pl.off_t, 64, a.batch * a.heads * pl.round * 256, 64))
+        !encode_gemm_2d(&tt, w + pl.off_t, 64, a.batch * a.heads * pl.round * mm::kGdrSolved, 64))
         return MM_ERR_CUDA;
     static std::atomic<unsigned long long> allowed_prep{0}, allowed_scan{0}, allowed_state{0}, allowed_segment{0};
     if (allow_smem(mm::gdr_prep_kernel<N>, allowed_prep) != cudaSuccess ||
