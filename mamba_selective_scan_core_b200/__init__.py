@@ -878,7 +878,7 @@ def gdr_fwd(q, k, v, dt, beta, dt_bias, A, h0=None, *, scale=None, norm_eps=1e-6
     G, N = q.shape[2:]
     tokens, keys, state = (Bsz, L, H), (Bsz, L, G, N), (Bsz, H, P, N)
     if not (idx >= 0 and q.dtype is dtype and k.dtype is dtype and q.get_device() == idx and k.get_device() == idx
-            and k.shape == keys and A is not None
+            and q.shape == keys and k.shape == keys and A is not None
             and dt.shape == tokens and dt.dtype is dtype and dt.get_device() == idx and dt.is_contiguous()
             and beta.shape == tokens and beta.dtype is dtype and beta.get_device() == idx and beta.is_contiguous()
             and A.shape == (H,) and A.dtype is f32 and A.get_device() == idx and A.is_contiguous()
@@ -959,7 +959,7 @@ def gdr_state_update(q, k, v, dt, beta, dt_bias, A, state, *, scale=None, norm_e
     G, N = q.shape[1:]
     tokens, keys = (Bsz, H), (Bsz, G, N)
     if not (idx >= 0 and q.dtype is dtype and k.dtype is dtype and q.get_device() == idx and k.get_device() == idx
-            and k.shape == keys and A is not None and state is not None
+            and q.shape == keys and k.shape == keys and A is not None and state is not None
             and dt.shape == tokens and dt.dtype is dtype and dt.get_device() == idx and dt.is_contiguous()
             and beta.shape == tokens and beta.dtype is dtype and beta.get_device() == idx and beta.is_contiguous()
             and A.shape == (H,) and A.dtype is f32 and A.get_device() == idx and A.is_contiguous()

@@ -1,0 +1,80 @@
+"""What the Python calls of the gated delta rule let through to the library,
+on the CPU: tensors that say they are on a device, and a library that counts
+its calls and runs nothing."""
+
+import pytest
+import torch
+
+import mamba_selective_scan_core_b200 as mm
+from gdr_ref import BF, F32, gdr_inputs
+from mamba_selective_scan_core_b200 import build as mmbuild
+
+
+class OnDevice(torch.Tensor):
+    is_cuda = True
+    device = torch.device("cuda", 0)
+
+    def get_device(self):
+        return 0
+
+
+class CountingLibrary:
+    def __init__(self):
+        self.calls = []
+
+    def mamba_gdr_workspace_size(self, *args):
+        return 256
+
+    def mamba_gdr_fwd(self, *args):
+        self.calls.append("fwd")
+        return 0
+
+    def mamba_gdr_state_update(self, *args):
+        self.calls.append("step")
+        return 0
+
+
+@pytest.fixture
+def library(monkeypatch):
+    mmbuild.build()
+    names = mm._names()
+    counting = CountingLibrary()
+    monkeypatch.setattr(names, "calls", None)
+    monkeypatch.setattr(names, "lib", counting)
+    monkeypatch.setattr(names, "current_device", lambda: 0)
+    monkeypatch.setattr(names, "raw_stream", lambda i: 0)
+    return counting
+
+
+def on_device(inp):
+    return {k: None if t is None else t.as_subclass(OnDevice) for k, t in inp.items()}
+
+
+def fwd(d, **kw):
+    return mm.gdr_fwd(d["q"], d["k"], d["v"], d["dt"], d["beta"], d["dt_bias"], d["A"], d["h0"], **kw)
+
+
+def step(d):
+    return mm.gdr_state_update(d["q"], d["k"], d["v"], d["dt"], d["beta"], d["dt_bias"], d["A"], d["h0"])
+
+
+@pytest.mark.parametrize("act", [BF, F32])
+@pytest.mark.parametrize("name", ["q", "k"])
+def test_sizes_of_q_and_k(library, act, name):
+    """q or k with fewer sequences or tokens than v, which the kernels would read past."""
+    d = on_device(gdr_inputs(3, 20, 1, 2, 64, 64, act))
+    fwd(d)
+    assert library.calls == ["fwd"]
+    for t in (d[name][:1], d[name][:2], d[name][:, :7], d[name][:1, :7].contiguous(), d[name][:, :7].contiguous(), d[name][:0]):
+        with pytest.raises(ValueError, match=name):
+            fwd(dict(d, **{name: t}))
+    one = on_device(gdr_inputs(3, None, 1, 2, 64, 64, act))
+    step(one)
+    for n in (0, 1, 2):
+        with pytest.raises(ValueError, match=name):
+            step(dict(one, **{name: one[name][:n]}))
+    single = on_device(gdr_inputs(1, 1, 1, 2, 64, 64, act))
+    fwd(single)
+    with pytest.raises(ValueError, match=name):
+        fwd(dict(single, **{name: single[name][:, :0]}))
+    assert library.calls == ["fwd", "step", "fwd"]
