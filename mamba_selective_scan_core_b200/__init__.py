@@ -925,6 +925,8 @@ def gdr_fwd(q, k, v, dt, beta, dt_bias, A, h0=None, *, scale=None, norm_eps=1e-6
         else:
             if workspace.get_device() != idx:
                 raise ValueError(f"workspace is on {workspace.device}, expected {v.device}")
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous")
             have = workspace.nbytes
         st = T.lib.mamba_gdr_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), beta.data_ptr(),
                                  None if dt_bias is None else dt_bias.data_ptr(), A.data_ptr(),

@@ -100,7 +100,7 @@ PyObject* gdr_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!activation(type) || B < 1 || qs < 0 || ks < 0 || vs < 0 || !dense(dt, dev, type, {B, L, H}) ||
         !dense(beta, dev, type, {B, L, H}) || !dense(A, dev, at::kFloat, {H}) || !dense_or_none(bias, dev, at::kFloat, {H}) ||
         !dense_or_none(h0, dev, at::kFloat, {B, H, P, N}) || !dense_or_none(y, dev, type, {B, L, H, P}) ||
-        !dense_or_none(h_last, dev, at::kFloat, {B, H, P, N}) || (ws && (!ws->is_cuda() || ws->get_device() != dev)) ||
+        !dense_or_none(h_last, dev, at::kFloat, {B, H, P, N}) || (ws && (!ws->is_cuda() || ws->get_device() != dev || !ws->is_contiguous())) ||
         !number(a[8], static_cast<float>(1.0 / std::sqrt(static_cast<double>(N))), scale) ||
         a[9] == Py_None || !number(a[9], 0.0f, eps))
         return none();

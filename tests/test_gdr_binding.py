@@ -78,3 +78,15 @@ def test_sizes_of_q_and_k(library, act, name):
     with pytest.raises(ValueError, match=name):
         fwd(dict(single, **{name: single[name][:, :0]}))
     assert library.calls == ["fwd", "step", "fwd"]
+
+
+def test_workspace_in_one_piece(library):
+    """A workspace whose bytes are not one block of memory (one byte expanded,
+    every other byte) is refused: its nbytes is not what lies behind its address."""
+    d = on_device(gdr_inputs(1, 20, 1, 2, 64, 64))
+    ws = torch.empty(4096, dtype=torch.uint8).as_subclass(OnDevice)
+    fwd(d, workspace=ws)
+    for bad in (ws[:1].expand(4096), ws[::2], ws.view(64, 64)[:, :32]):
+        with pytest.raises(ValueError, match="workspace"):
+            fwd(d, workspace=bad)
+    assert library.calls == ["fwd"]
