@@ -59,10 +59,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* gsrc, uint32_t 
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n"
                  :: "r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(bytes), "r"(smem_addr(bar)) : "memory");
 }
-// the same answer for every lane of the warp
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned limit) {
-    return __all_sync(kFull, mbar_wait_bounded(bar, parity, limit));
-}
 
 // ---------------------------------------------------------------- token by token
 // State rows stay in registers for the whole call.  Eight lanes hold a row,

@@ -173,6 +173,13 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, unsigned parity
         if (mbar_try_wait(bar, parity)) return true;
     return false;
 }
+// The same wait by a whole warp, with one answer for all its lanes.  Each lane
+// counts its own tries, so a phase that completes between two lanes' last ones
+// would send them different ways; what a warp does together after a wait
+// (mma.sync, tensor memory, a full-mask shuffle) takes this.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned limit) {
+    return __all_sync(kFull, mbar_wait_bounded(bar, parity, limit));
+}
 // Programmatic dependent launch.  launch_dependents lets the next kernel in
 // the stream, when launched as a programmatic dependent, start once every CTA
 // of this grid has executed it (or exited).  grid_dependency_wait returns once

@@ -216,7 +216,7 @@ proj_q4_kernel(const Q4Params p, const __grid_constant__ CUtensorMap tm_w, const
                 z1[q] = ZEROS ? 8.0f - __bfloat162float(zc[d][1][q]) : 0.0f;
             }
             fetch(i + kAhead, d);
-            if (!mbar_wait_bounded(&full[s], static_cast<unsigned>((i / Lay::stages) & 1), p.wait_limit)) {
+            if (!warp_wait(&full[s], static_cast<unsigned>((i / Lay::stages) & 1), p.wait_limit)) {
                 ok = false;
                 break;
             }

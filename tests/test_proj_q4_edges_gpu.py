@@ -1,0 +1,32 @@
+"""The projection with 4-bit weights where its calls end: waits that give up
+part of the way, the longest rows, inputs that are not finite."""
+
+import pytest
+import torch
+
+import mamba_selective_scan_core_b200 as mm
+from gdr_ref import BF, F32, q4_inputs, q4_reference
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("M,N,K,group,zeros", [(1, 1000, 8192, 128, False), (20, 300, 4096, 32, True)])
+def test_waits_that_give_up_part_of_the_way(monkeypatch, M, N, K, group, zeros):
+    """Waits of a few tries, which some warps get through and others do not: a
+    call is either right or reported, and the next one is right."""
+    d = {k: None if t is None else t.cuda() for k, t in q4_inputs(M, N, K, group, seed=M, zeros=zeros).items()}
+    args = (d["x"], d["W"], d["scales"], d["zeros"])
+    want = mm.proj_q4(*args, group=group)
+    torch.cuda.synchronize()
+    assert mm.fault_status(reset=True) == 0
+    for limit in (1, 2, 3, 4, 6, 8, 12, 16, 32):
+        for _ in range(20):
+            monkeypatch.setenv("MAMBA_MIXER_WAIT_LIMIT", str(limit))
+            got = mm.proj_q4(*args, group=group)
+            torch.cuda.synchronize()
+            monkeypatch.delenv("MAMBA_MIXER_WAIT_LIMIT")
+            status = mm.fault_status(reset=True)
+            assert status in (0, 11)
+            if status == 0:
+                assert torch.equal(got, want)
+    assert torch.equal(mm.proj_q4(*args, group=group), want) and mm.fault_status() == 0
