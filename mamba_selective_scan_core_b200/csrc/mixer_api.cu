@@ -2224,13 +2224,13 @@ cudaError_t launch_q4_t(mm::Q4Params p, const void* x, const void* W, cudaStream
     if (cudaError_t e = allow_smem(kern, smem_allowed); e != cudaSuccess) return e;
     // K is split over a cluster until the grid covers the SMs or a CTA has two
     // slots (three CTAs a SM took 16.2 us where this takes 14.7: 16384 x 4096)
-    const int64_t tiles = (static_cast<int64_t>(p.N) + mm::kQ4Rows - 1) / mm::kQ4Rows * ((p.M + MT * 8 - 1) / (MT * 8));
-    const int slots = (p.K + mm::kQ4K - 1) / mm::kQ4K;
+    const int64_t tiles = static_cast<int64_t>((p.N - 1) / mm::kQ4Rows + 1) * ((p.M + MT * 8 - 1) / (MT * 8));
+    const int slots = (p.K - 1) / mm::kQ4K + 1;      // K and N may be as large as an int gets
     int split = 1;
     while (split < 8 && tiles * split < plan_sms() && slots >= 4 * split) split *= 2;
     p.slots_per_cta = (slots + split - 1) / split;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((p.N + mm::kQ4Rows - 1) / mm::kQ4Rows),
+    cfg.gridDim = dim3(static_cast<unsigned>((p.N - 1) / mm::kQ4Rows + 1),
                        static_cast<unsigned>((p.M + MT * 8 - 1) / (MT * 8)), static_cast<unsigned>(split));
     cfg.blockDim = dim3(mm::kQ4Threads);
     cfg.dynamicSmemBytes = forced_launch_failure() ? size_t(1) << 20 : static_cast<size_t>(mm::Q4Layout<MT>::smem_bytes);

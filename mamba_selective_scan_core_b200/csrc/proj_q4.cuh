@@ -129,7 +129,7 @@ proj_q4_kernel(const Q4Params p, const __grid_constant__ CUtensorMap tm_w, const
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n0 = blockIdx.x * kQ4Rows, m0 = blockIdx.y * MT * 8;
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
-    const int slots_all = (p.K + kQ4K - 1) / kQ4K;
+    const int slots_all = (p.K - 1) / kQ4K + 1;
     const int slot0 = static_cast<int>(rank) * p.slots_per_cta;
     const int slots = max(0, min(p.slots_per_cta, slots_all - slot0));
 

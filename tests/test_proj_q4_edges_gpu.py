@@ -30,3 +30,20 @@ def test_waits_that_give_up_part_of_the_way(monkeypatch, M, N, K, group, zeros):
             if status == 0:
                 assert torch.equal(got, want)
     assert torch.equal(mm.proj_q4(*args, group=group), want) and mm.fault_status() == 0
+
+
+def test_the_longest_row():
+    """K = 2^31 - 32, the largest that the call takes: a few inputs of one row,
+    the last among them, whose sum is exact."""
+    K = 2 ** 31 - 32
+    x = torch.zeros(1, K, dtype=BF, device="cuda")
+    W = torch.zeros(1, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.ones(1, K // 32, dtype=BF, device="cuda")
+    want = 0.0
+    for k, v, c in ((0, 1.0, 15), (255, 0.5, 3), (2 ** 30 + 5, 2.0, 11), (K - 33, -4.0, 1), (K - 1, 8.0, 13)):
+        x[0, k] = v
+        W[0, k // 2] = c << 4 if k % 2 else c
+        want += v * (c - 8)
+    out = mm.proj_q4(x, W, scales, group=32)
+    torch.cuda.synchronize()
+    assert out.item() == want
