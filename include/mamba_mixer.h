@@ -683,7 +683,8 @@ mm_status mamba_gdr_state_update(const void* q, const void* k, const void* v, co
  *   out     [M, N]          fp32 (out_dtype MM_F32) or bf16 (MM_BF16, rounded to nearest even)
  *
  * Sums are fp32; c - 8 and x enter the products exactly and each group's sum
- * is scaled.  group is 32, 64 or 128 (MM_ERR_UNSUPPORTED otherwise) and
+ * is scaled.  Infinities and NaN in x give what the formula gives; scales and
+ * zero points are finite.  group is 32, 64 or 128 (MM_ERR_UNSUPPORTED otherwise) and
  * divides K (MM_ERR_SHAPE); M <= 64 * 65535, N and K below 2^31.  Any M runs;
  * the weight is read once per 64 rows, so mamba_proj_matmul suits a long
  * prompt better.  Every pointer 16-byte aligned (MM_ERR_ALIGN); out may not

@@ -2281,6 +2281,8 @@ mm_status mamba_proj_q4(const void* x, const void* W, const void* scales, const 
         return MM_ERR_ALIAS;
     if (mm_status st = check_device(); st != MM_OK) return st;
     mm::Q4Params p{};
+    p.x = static_cast<const __nv_bfloat16*>(x);
+    p.W = static_cast<const unsigned char*>(W);
     p.scales = static_cast<const __nv_bfloat16*>(scales);
     p.zeros = static_cast<const __nv_bfloat16*>(zeros);
     p.out = out;

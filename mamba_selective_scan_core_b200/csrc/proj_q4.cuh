@@ -22,7 +22,8 @@
 // c - 8 is exact in bf16, and so is x; products and their sums over a group
 // are fp32, and the scale is applied to a group's sum, so nothing is rounded
 // to fewer bits before the output.  The zero point's part is
-// s (8 - z) sum_k x[m, k], whose sum is one more mma with a matrix of ones.
+// s (8 - z) sum_k x[m, k], whose sum is one more mma with a matrix of ones; an
+// output that is not finite is worked out again term by term.
 //
 // What bounds it: the integer pipe.  A product's 16 x 128 weights take 32
 // mask-and-ors, 24 shifts and 16 byte permutes there, at two cycles each; in
@@ -50,6 +51,8 @@ constexpr int kQ4Consumers = 8;       // warps: 4 groups of 16 outputs x 2 halve
 constexpr int kQ4Threads = 32 * (kQ4Consumers + 1);
 
 struct Q4Params {
+    const __nv_bfloat16* x;        // [M][K]
+    const unsigned char* W;        // [N][K / 2]
     const __nv_bfloat16* scales;   // [N][K / G]
     const __nv_bfloat16* zeros;    // [N][K / G] or null (8)
     void* out;                     // [M][N] fp32 or bf16
@@ -89,6 +92,24 @@ __device__ __forceinline__ void load_pair(const unsigned char* p, uint32_t* v) {
     const uint2 w = *reinterpret_cast<const uint2*>(p);
     v[0] = w.x;
     v[1] = w.y;
+}
+
+// One output term by term, as the formula has it.
+__device__ __noinline__ float q4_formula(const Q4Params& p, int m, int n, int words) {
+    const int groups = p.K / (8 * words);
+    const __nv_bfloat16* x = p.x + static_cast<int64_t>(m) * p.K;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(p.W + static_cast<int64_t>(n) * (p.K / 2));
+    const int64_t row = static_cast<int64_t>(n) * groups;
+    float sum = 0.0f;
+    for (int q = 0; q < groups && sum == sum; ++q) {        // a NaN stays one
+        const float z = __bfloat162float(p.zeros[row + q]);
+        float part = 0.0f;
+        for (int j = 0; j < words; ++j, ++w)
+            for (int i = 0; i < 8; ++i, ++x)
+                part = fmaf(__bfloat162float(*x), static_cast<float>((*w >> (4 * i)) & 15u) - z, part);
+        sum = fmaf(__bfloat162float(p.scales[row + q]), part, sum);
+    }
+    return sum;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -332,6 +353,10 @@ proj_q4_kernel(const Q4Params p, const __grid_constant__ CUtensorMap tm_w, const
             } else {
                 v = r[0] + r[MT * 8 * Lay::red_ld];
             }
+            // An infinity among x: its part of the two sums may be of either
+            // sign, or 0 times it, and they make NaN of what the formula has
+            // as an infinity.  Rare enough to be worked out from the start.
+            if (ZEROS && !(fabsf(v) <= 3.402823466e38f)) v = q4_formula(p, m0 + m, n0 + n, 4 * GB);
             const int64_t o = static_cast<int64_t>(m0 + m) * p.N + n0 + n;
             if constexpr (OUT_BF16) static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(v);
             else static_cast<float*>(p.out)[o] = v;

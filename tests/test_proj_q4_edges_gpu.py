@@ -47,3 +47,34 @@ def test_the_longest_row():
     out = mm.proj_q4(x, W, scales, group=32)
     torch.cuda.synchronize()
     assert out.item() == want
+
+
+@pytest.mark.parametrize("M", [1, 3, 12, 20, 40])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zeros,fractional", [(False, False), (True, False), (True, True)])
+def test_inputs_that_are_not_finite(M, group, zeros, fractional):
+    """Infinities and NaN in some rows of x: what the formula gives, infinity
+    times c - z of either sign and NaN where that is 0; the other rows as ever."""
+    K, N = 640, 70
+    inp = q4_inputs(M, N, K, group, seed=M + group, zeros=zeros, fractional=fractional)
+    inp["scales"] = inp["scales"].abs() + 0.01
+    x, inf = inp["x"], float("inf")
+    x[0, 5] = inf
+    if M > 1:
+        x[2, 300], x[2, K - 1] = -inf, -inf
+    if M > 8:
+        x[8, 7], x[8, 70], x[M - 1, 33], x[M - 2, 0], x[M - 2, 1] = inf, -inf, float("nan"), inf, -inf
+    d = {k: None if t is None else t.cuda() for k, t in inp.items()}
+    out = mm.proj_q4(d["x"], d["W"], d["scales"], d["zeros"], group=group).cpu().double()
+    W = inp["W"].to(torch.int64)
+    c = torch.stack([W & 15, W >> 4], -1).reshape(N, -1, group).double()
+    z = 8.0 if inp["zeros"] is None else inp["zeros"].double()[..., None]
+    w = ((c - z) * inp["scales"].double()[..., None]).reshape(N, K)
+    ref = (x.double()[:, None, :] * w).sum(-1)
+    odd = [m for m in range(M) if not torch.isfinite(x[m]).all()]
+    assert torch.equal(out[odd].isnan(), ref[odd].isnan())
+    assert torch.equal(out[odd].nan_to_num(nan=0.0), ref[odd].nan_to_num(nan=0.0))
+    if M > 1:
+        rest = [m for m in range(M) if m not in odd]
+        clean, mag = q4_reference(dict(inp, x=x[rest]), group)
+        assert ((out[rest] - clean).abs() <= (K / 4 + 32) * 2.0 ** -24 * mag + 2.0 ** -24 * clean.abs()).all()
