@@ -621,6 +621,11 @@ mm_status mamba_m3_state_update(const void* x, const void* z, const void* dt, co
  * state as it is, whatever finite q, k and v it has; sequences of different
  * lengths run as one batch that way (the padding's y is still written).
  *
+ * An input that is not finite (a beta of +-inf and a dt of +-inf are as the
+ * formulas have them) leaves every output and state that it does not reach as
+ * it is, the tokens before it among them; what it reaches is not finite, NaN
+ * where the formulas may have an infinity.
+ *
  * bf16 calls of more than some tens of tokens run in chunks of 64 as dense
  * products on the tensor cores, what they compute of their operands in three
  * bf16 parts (26 bits), sums and the state in fp32; long ones of few

@@ -527,6 +527,12 @@ gdr_tokens_kernel(const GdrParams p, const __grid_constant__ CUtensorMap tm_q, c
 // in fp64 and kept as two floats: the sums reach hundreds, the differences of
 // neighbours matter.  A token's Delta A is held above -200 (exp(-200) is 0 in
 // fp32, so nothing changes) to keep the sums finite.
+//
+// A product takes whole rows, zeros of T and M among them, and 0 x NaN would
+// carry a token that is not finite to those before it.  So the kernels keep
+// such values out of T and X (0 in their place), remember the first token from
+// which a channel is not finite, and put NaN into its u' and y from there on (12 us of
+// 356).
 constexpr int kGdrC = 64;             // tokens per chunk
 constexpr int kGdrTile = 64;          // state rows per CTA of the scan
 constexpr int kGdrFac = 5 * kGdrC;    // factors of a chunk
@@ -555,6 +561,9 @@ struct GdrChunkParams {
     unsigned long long* status;
     unsigned long long status_epoch;
 };
+
+__device__ __forceinline__ bool is_finite(float v) { return fabsf(v) <= 3.402823466e38f; }
+__device__ __forceinline__ float nan32() { return __uint_as_float(0x7fffffffu); }
 
 __device__ __forceinline__ void gdr_fail(const GdrChunkParams& p) {
     atomicOr(&g_mm_fault, 1u);
@@ -687,6 +696,7 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     float* rk = bt + kGdrC;                              // 1 / |k_t| or 1
     float* rq = rk + kGdrC;                              // scale / |q_t| or scale
     double* half_sum = reinterpret_cast<double*>(rq + kGdrC);
+    int* bad = reinterpret_cast<int*>(half_sum + 1);     // the first token whose row of L is not finite
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Lay::bar_off);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3);
 
@@ -699,6 +709,7 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     if (p.status && tid == 0 && c == 0 && h == 0 && b == 0) p.status[1] = p.status_epoch;
 
     if (tid == 7 * 32) {
+        *bad = kGdrC;
         mbar_init(&bars[0], 1);
         mbar_init(&bars[1], 1);
         mbar_init(&bars[2], 1);
@@ -716,6 +727,7 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     }
     // decays and write strengths; a token past the sequence has a = 1, b = 0
     double cum = 0.0;
+    bool fine = true;
     if (tid < kGdrC) {
         float la = 0.0f, be = 0.0f;
         if (t0 + tid < p.L) {
@@ -731,9 +743,11 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
             if (lane >= o) cum += n;
         }
         if (tid == 31) *half_sum = cum;
-        bt[tid] = be;
+        fine = is_finite(la) && is_finite(be);
+        bt[tid] = is_finite(be) ? be : 0.0f;
     }
     __syncthreads();
+    if (!fine) atomicMin(bad, tid);
     if (tid < kGdrC) {
         if (warp == 1) cum += *half_sum;
         const float hi = static_cast<float>(cum);
@@ -798,19 +812,15 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) m[e] = 0.0f;
-            if (key) {
-                // this warp has no columns of L: the tokens' factors instead
-                // (row i < 32; its lanes take tokens i and i + 32)
+        }
+        if (key) {
+            float odd = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int t = lane + 32 * k;
-                    const float gam = ex2_fast(cum_hi[t] + cum_lo[t]);
-                    const float end = ex2_fast((cum_hi[kGdrC - 1] - cum_hi[t]) + (cum_lo[kGdrC - 1] - cum_lo[t]));
-                    float* fac = p.fac + unit * kGdrFac;
-                    *reinterpret_cast<float4*>(fac + 4 * t) = make_float4(gam * rk[t], end * rk[t], gam * rq[t],
-                                                                          ex2_fast(cum_hi[kGdrC - 1] + cum_lo[kGdrC - 1]));
-                    fac[4 * kGdrC + t] = bt[t];
-                }
+            for (int e = 0; e < 32; ++e) odd = fmaf(m[e], 0.0f, odd);
+            if (odd != 0.0f) {
+                atomicMin(bad, i);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) m[e] = is_finite(m[e]) ? m[e] : 0.0f;
             }
         }
         if (key) {
@@ -856,6 +866,16 @@ gdr_prep_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         // zeros right of the diagonal blocks
         const int i = tid - kGdrC;
         for (int j = (i / 16 + 1) * 16; j < kGdrC; j += 4) *reinterpret_cast<float4*>(Tm + i * ld + j) = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else if (ready && tid < 3 * kGdrC) {
+        // the tokens' factors; from the first token whose row of L is not
+        // finite on, one that makes X what its u is
+        const int t = tid - 2 * kGdrC;
+        const float gam = ex2_fast(cum_hi[t] + cum_lo[t]);
+        const float end = ex2_fast((cum_hi[kGdrC - 1] - cum_hi[t]) + (cum_lo[kGdrC - 1] - cum_lo[t]));
+        float* fac = p.fac + unit * kGdrFac;
+        *reinterpret_cast<float4*>(fac + 4 * t) = make_float4(t < *bad ? gam * rk[t] : nan32(), end * rk[t], gam * rq[t],
+                                                              ex2_fast(cum_hi[kGdrC - 1] + cum_lo[kGdrC - 1]));
+        fac[4 * kGdrC + t] = bt[t];
     }
     __syncthreads();
     // W lies in L's upper right block, which nothing reads
@@ -989,7 +1009,8 @@ struct GdrScanLayout {
     static_assert(x_bytes <= s_bytes, "X's parts fit S's place");
     static constexpr int bar_off = s_off + 3 * s_bytes;
     static constexpr int bars = 2 * stages + 8;
-    static constexpr int smem_bytes = 1024 + bar_off + bars * 8 + 16;
+    static constexpr int odd_off = bar_off + bars * 8 + 16;     // the first token from which each row is not finite, and whether any is not
+    static constexpr int smem_bytes = 1024 + odd_off + (kGdrTile + 4) * 4;
 };
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -1059,6 +1080,8 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
     uint64_t* d_full = t_free + 1;                       // [3] products 1, 2, 3
     uint64_t* in_full = d_full + 3;                      // [3] S, X, u' written
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + 3);
+    int* odd_from = reinterpret_cast<int*>(sm + Lay::odd_off);
+    volatile int* any_odd = odd_from + kGdrTile;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int segs = STATE ? p.segs - 1 : p.segs;
@@ -1082,7 +1105,9 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
         mbar_init(&in_full[1], kGdrWarps / 2);
         mbar_init(&in_full[2], kGdrWarps);
         fence_mbar_init();
+        *any_odd = 0;
     }
+    if (tid < kGdrTile) odd_from[tid] = 0x7fffffff;
     // What the kernels before wrote is read from here on.  All of tensor memory
     // is allocated after that, too: a block of theirs that has yet to allocate
     // could otherwise wait for this one, and this one for it.
@@ -1209,6 +1234,12 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
             __syncwarp();
             if (elect_one_lane()) mbar_arrive(bar);
         };
+        // whether any value of this chunk or one before it is not finite; the
+        // keys' warps have said so before they arrived there
+        auto is_odd = [&](unsigned parity) {
+            mbar_try_wait(&in_full[1], parity);
+            return *any_odd != 0;
+        };
         // this thread's part of an operand is written: to the products
         auto hand_over = [&](uint64_t* bar) {
             fence_proxy_async_smem();
@@ -1250,18 +1281,29 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 tc_fence_after();
                 float x[16];
                 tmem_ld_sum<16, 3>(lane_base + kD1 + col0, x);
+                float2 odd = f2(0.0f, 0.0f);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const uint32_t off = sw128_off(i, wg * 2 + k);
                     const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float2 r = fma2(f2(-f.x, -f.x), f2(x[8 * k + 2 * e], x[8 * k + 2 * e + 1]), f2(bf16_lo(w[e]), bf16_hi(w[e])));
                         x[8 * k + 2 * e] = r.x;
                         x[8 * k + 2 * e + 1] = r.y;
+                        odd = fma2(r, f2(0.0f, 0.0f), odd);
                     }
-                    split3_store8(x + 8 * k, xp + off, Lay::x_bytes);
                 }
+                if (odd.x + odd.y != 0.0f) {
+                    *any_odd = 1;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (!is_finite(x[e])) {
+                            atomicMin(odd_from + col0 + e, c * kGdrC + i);
+                            x[e] = 0.0f;
+                        }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) split3_store8(x + 8 * k, xp + sw128_off(i, wg * 2 + k), Lay::x_bytes);
                 hand_over(&in_full[1]);
                 if (!wait(&d_full[1], par)) break;
                 tc_fence_after();
@@ -1269,7 +1311,6 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                 tmem_ld_sum<16, 3>(lane_base + kD2 + col0, u);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const uint32_t off = sw128_off(i, wg * 2 + k);
 #pragma unroll
                     for (int e = 0; e < 8; e += 2) {
                         const float2 r = mul2(f2(f.y, f.y), fma2(f2(bi, bi), f2(x[8 * k + e], x[8 * k + e + 1]),
@@ -1277,8 +1318,12 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                         u[8 * k + e] = r.x;
                         u[8 * k + e + 1] = r.y;
                     }
-                    split3_store8(u + 8 * k, xp + off, Lay::x_bytes);
                 }
+                if (is_odd(par))
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) u[e] = odd_from[col0 + e] <= c * kGdrC + i ? nan32() : u[e];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) split3_store8(u + 8 * k, xp + sw128_off(i, wg * 2 + k), Lay::x_bytes);
                 hand_over(&in_full[2]);
                 if (!wait(&d_full[2], par)) break;
                 tc_fence_after();
@@ -1318,6 +1363,11 @@ gdr_scan_kernel(const GdrChunkParams p, const __grid_constant__ CUtensorMap tm_q
                         const float2 r = fma2(f2(f.z, f.z), f2(d[2 * e], d[2 * e + 1]), f2(u[2 * e], u[2 * e + 1]));
                         yw[e] = pack_bf16x2(r.x, r.y);
                     }
+                    if (is_odd(par))
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            yw[e] |= (odd_from[col0 + 2 * e] <= c * kGdrC + i ? 0x7fffu : 0u) |
+                                     (odd_from[col0 + 2 * e + 1] <= c * kGdrC + i ? 0x7fff0000u : 0u);
                 }
                 if (!wait(&d_full[2], par)) break;
                 tc_fence_after();
