@@ -1952,6 +1952,23 @@ bool encode_gdr_rows(CUtensorMap* m, const void* base, bool bf16, int64_t cols, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// `count` sequences of a bf16 call, from the b0-th on
+GdrArgs gdr_sequences(const GdrArgs& a, int64_t b0, int64_t count) {
+    GdrArgs p = a;
+    auto skip = [](const void* q, int64_t elements) { return static_cast<const __nv_bfloat16*>(q) + elements; };
+    const int64_t tokens = b0 * a.seqlen, state = b0 * a.heads * a.headdim * a.d_state;
+    p.batch = count;
+    p.q = skip(a.q, tokens * a.q_stride);
+    p.k = skip(a.k, tokens * a.k_stride);
+    p.v = skip(a.v, tokens * a.v_stride);
+    p.dt = skip(a.dt, tokens * a.heads);
+    p.beta = skip(a.beta, tokens * a.heads);
+    p.y = static_cast<__nv_bfloat16*>(a.y) + tokens * a.heads * a.headdim;
+    p.h0 = a.h0 ? a.h0 + state : nullptr;
+    p.h_last = a.h_last + state;
+    return p;
+}
+
 // RPT: state rows a lane of the 128 threads that hold the state
 template <int RPT>
 dim3 gdr_rows_grid(const mm::GdrParams& p, int64_t batch) {
@@ -1996,15 +2013,18 @@ mm_status launch_gdr_recurrent(const mm::GdrParams& p, const GdrArgs& a, cudaStr
 // The chunked form: bf16 calls of enough tokens.  One chunk costs 13 us (two
 // dependent kernels, the triangular system between them); token by token, a
 // block of 8 tokens costs 1.3 to 2.2 us while the state's rows leave the SMs
-// free (crossing at 41 to 62 tokens), 14 us with 32768 rows of 128 (at 11).  The chunks run in rounds of as many as bring the workspace
-// to kGdrRoundUnits chunks of a head, each round from the state that the one
-// before left in the workspace (two of them in turn: a round's first segment
-// reads one while its last writes the other).
+// free (crossing at 41 to 62 tokens), 14 us with 32768 rows of 128 (at 11).
+// The workspace is kept to kGdrRoundUnits chunks of a head (of a sequence's
+// heads, where it has more): the sequences go in parts, one after another, and
+// a part's chunks in rounds of as many as that allows, each round from the
+// state that the one before left in the workspace (two of them in turn: a
+// round's first segment reads one while its last writes the other).
 constexpr int64_t kGdrManyRows = 16384;        // state rows of all heads
 int64_t gdr_chunked_min(int64_t rows) { return rows >= kGdrManyRows ? 16 : 44; }
 constexpr int64_t kGdrRoundUnits = 16384;      // 50 KB each
 struct GdrPlan {
     bool chunked = false;
+    int64_t part = 0;                          // sequences at a time
     int64_t chunks = 0, round = 0;             // of a sequence; of a launch
     int segs = 1;                              // of a launch's chunks, at most
     size_t off_fac = 0, off_t = 0, off_out = 0, off_in = 0, off_carry = 0, total = kWsHeader;
@@ -2032,19 +2052,21 @@ int gdr_segments(int64_t batch, int64_t tiles, int64_t trans_tiles, int64_t chun
 }
 GdrPlan plan_gdr(int64_t batch, int64_t seqlen, int64_t heads, int64_t headdim, int64_t d_state, mm_dtype act, int64_t sms) {
     GdrPlan pl;
-    if (act != MM_BF16 || seqlen < gdr_chunked_min(batch * heads * headdim) || batch * heads > (int64_t(1) << 20)) return pl;
+    if (act != MM_BF16 || seqlen < gdr_chunked_min(batch * heads * headdim)) return pl;
     pl.chunked = true;
+    const int64_t most = std::max<int64_t>(1, kGdrRoundUnits / heads), parts = (batch + most - 1) / most;
+    pl.part = (batch + parts - 1) / parts;
     pl.chunks = (seqlen + mm::kGdrC - 1) / mm::kGdrC;
-    pl.round = std::min(pl.chunks, std::max<int64_t>(1, kGdrRoundUnits / (batch * heads)));
-    const int64_t units = batch * heads * pl.round;
+    pl.round = std::min(pl.chunks, std::max<int64_t>(1, kGdrRoundUnits / (pl.part * heads)));
+    const int64_t units = pl.part * heads * pl.round;
     pl.off_fac = kWsHeader;
     pl.off_t = pl.off_fac + static_cast<size_t>(units) * mm::kGdrFac * 4;
     pl.off_out = pl.off_t + static_cast<size_t>(units) * mm::kGdrSolved * 128;
-    pl.segs = gdr_segments(batch, batch * heads * headdim / mm::kGdrTile, batch * heads * d_state / mm::kGdrTile, pl.round, sms);
-    const int64_t rows = batch * heads * (pl.segs - 1) * d_state;
+    pl.segs = gdr_segments(pl.part, pl.part * heads * headdim / mm::kGdrTile, pl.part * heads * d_state / mm::kGdrTile, pl.round, sms);
+    const int64_t rows = pl.part * heads * (pl.segs - 1) * d_state;
     pl.off_in = pl.off_out + static_cast<size_t>(rows * (headdim + d_state)) * 4;
     pl.off_carry = pl.off_in + static_cast<size_t>(rows * headdim) * 4;
-    pl.total = pl.off_carry + (pl.round < pl.chunks ? static_cast<size_t>(batch * heads * headdim * d_state) * 8 : 0);
+    pl.total = pl.off_carry + (pl.round < pl.chunks ? static_cast<size_t>(pl.part * heads * headdim * d_state) * 8 : 0);
     return pl;
 }
 
@@ -2170,7 +2192,13 @@ mm_status mamba_gdr_fwd(const void* q, const void* k, const void* v, const void*
     if (pl.chunked) {
         unsigned char* w = static_cast<unsigned char*>(workspace);
         cudaStream_t s = static_cast<cudaStream_t>(stream);
-        return d_state == 64 ? launch_gdr_chunked<64>(a, pl, w, epoch, s) : launch_gdr_chunked<128>(a, pl, w, epoch, s);
+        for (int64_t b0 = 0; b0 < batch; b0 += pl.part) {
+            const GdrArgs part = gdr_sequences(a, b0, std::min(pl.part, batch - b0));
+            const mm_status st = d_state == 64 ? launch_gdr_chunked<64>(part, pl, w, epoch, s)
+                                               : launch_gdr_chunked<128>(part, pl, w, epoch, s);
+            if (st != MM_OK) return st;
+        }
+        return MM_OK;
     }
     mm::GdrParams p = gdr_params(a);
     p.status = static_cast<unsigned long long*>(workspace);

@@ -90,3 +90,16 @@ def test_workspace_in_one_piece(library):
         with pytest.raises(ValueError, match="workspace"):
             fwd(d, workspace=bad)
     assert library.calls == ["fwd"]
+
+
+@pytest.mark.parametrize("B,L,H,P,N", [(1024, 64, 128, 64, 64), (65535, 100, 16, 64, 64), (300, 4096, 64, 128, 128), (8, 70, 65535, 64, 64),
+                                       (1, 1 << 20, 4096, 64, 128)])
+def test_workspace_is_bounded(B, L, H, P, N):
+    """However many sequences: 50 KB for each of 16384 chunks of a head (or one
+    of each head, where a sequence has more), two states of the heads at work
+    where their chunks take several rounds, and a segment's states and
+    transitions for the few heads of calls that have segments."""
+    units = max(16384, H)
+    bound = 256 + units * (5 * 64 * 4 + 6 * 64 * 128) + 2 * units * P * N * 4 + 32 * 256 * (2 * P + N) * N * 4
+    assert 256 < mm.gdr_workspace_size(B, L, H, P, N, 1) <= bound
+    assert mm.gdr_workspace_size(B, L, H, P, N, 1) <= mm.gdr_workspace_size(B, 4 * L, H, P, N, 1)
