@@ -826,6 +826,7 @@ class _Torch:
         self.f32, self.bf16, self.u8 = torch.float32, torch.bfloat16, torch.uint8
         self.codes = {torch.float32: MM_F32, torch.bfloat16: MM_BF16}
         self.device, self.current_device = torch.cuda.device, torch.cuda.current_device
+        self.on, self.current_stream = torch.cuda.stream, torch.cuda.current_stream
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda i: torch.cuda.current_stream(i).cuda_stream)
         self.lib = lib()
@@ -840,6 +841,20 @@ class _Torch:
                 self.lib.mamba_gdr_fwd, self.lib.mamba_gdr_workspace_size, self.lib.mamba_gdr_state_update,
                 self.lib.mamba_proj_q4)))
             self.calls = _calls
+
+
+    def empty(self, like, shape, dtype, stream, given_back=True):
+        """Memory for a call that runs on `stream`: torch's allocator hands out
+        what was freed on a stream to that stream while its work may still be
+        running, so the memory is taken there and not on the current stream --
+        which is told to the allocator where the caller gets the tensor."""
+        if stream is None:
+            return like.new_empty(shape, dtype=dtype)
+        with self.on(stream):
+            t = like.new_empty(shape, dtype=dtype)
+        if given_back:
+            t.record_stream(self.current_stream(t.device))
+        return t
 
 
 _torch_names = None
@@ -910,18 +925,14 @@ def gdr_fwd(q, k, v, dt, beta, dt_bias, A, h0=None, *, scale=None, norm_eps=1e-6
         with T.device(idx):
             return gdr_fwd(q, k, v, dt, beta, dt_bias, A, h0, scale=scale, norm_eps=norm_eps, y=y, h_last=h_last,
                            workspace=workspace, stream=stream)
-    made = []
     if y is None:
-        y = v.new_empty((Bsz, L, H, P))
-        made.append(y)
+        y = T.empty(v, (Bsz, L, H, P), dtype, stream)
     if h_last is None:
-        h_last = A.new_empty(state)
-        made.append(h_last)
+        h_last = T.empty(v, state, f32, stream)
     while True:
         if workspace is None:
             have = max(T.lib.mamba_gdr_workspace_size(Bsz, L, H, P, N, G, act), 256)
-            workspace = v.new_empty(have, dtype=T.u8)
-            made.append(workspace)
+            workspace = T.empty(v, (have,), T.u8, stream, given_back=False)
         else:
             if workspace.get_device() != idx:
                 raise ValueError(f"workspace is on {workspace.device}, expected {v.device}")
@@ -938,8 +949,6 @@ def gdr_fwd(q, k, v, dt, beta, dt_bias, A, h0=None, *, scale=None, norm_eps=1e-6
         if st != _ERR_WORKSPACE or have >= T.lib.mamba_gdr_workspace_size(Bsz, L, H, P, N, G, act):
             raise MixerError(st, "mamba_gdr_fwd")
         workspace = None          # the one given is too small
-    if stream is not None:
-        _keep_alive_on(made, (stream,))
     return y, h_last
 
 
@@ -987,17 +996,14 @@ def gdr_state_update(q, k, v, dt, beta, dt_bias, A, state, *, scale=None, norm_e
     if T.current_device() != idx:
         with T.device(idx):
             return gdr_state_update(q, k, v, dt, beta, dt_bias, A, state, scale=scale, norm_eps=norm_eps, y=y, stream=stream)
-    own = y is None
-    if own:
-        y = v.new_empty((Bsz, H, P))
+    if y is None:
+        y = T.empty(v, (Bsz, H, P), dtype, stream)
     st = T.lib.mamba_gdr_state_update(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), beta.data_ptr(),
                                       None if dt_bias is None else dt_bias.data_ptr(), A.data_ptr(), state.data_ptr(),
                                       y.data_ptr(), Bsz, G, H, P, N, qs, ks, vs, N ** -0.5 if scale is None else scale,
                                       norm_eps, act, T.raw_stream(idx) if stream is None else stream.cuda_stream)
     if st != 0:
         raise MixerError(st, "mamba_gdr_state_update")
-    if own and stream is not None:
-        y.record_stream(stream)
     return y
 
 
@@ -1034,13 +1040,10 @@ def proj_q4(x, W, scales, zeros=None, *, group=128, out=None, out_dtype=None, st
     if T.current_device() != idx:
         with T.device(idx):
             return proj_q4(x, W, scales, zeros, group=group, out=out, out_dtype=out_dtype, stream=stream)
-    own = out is None
-    if own:
-        out = x.new_empty((M, N), dtype=dtype)
+    if out is None:
+        out = T.empty(x, (M, N), dtype, stream)
     st = T.lib.mamba_proj_q4(x.data_ptr(), W.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
                              out.data_ptr(), M, N, K, group, code, T.raw_stream(idx) if stream is None else stream.cuda_stream)
     if st != 0:
         raise MixerError(st, "mamba_proj_q4")
-    if own and stream is not None:
-        out.record_stream(stream)
     return out
