@@ -13,12 +13,12 @@
 
 #include <algorithm>
 #include <cmath>
-#include <exception>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "mamba_mixer.h"
@@ -185,17 +185,13 @@ PyObject* proj_q4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return made.defined() ? THPVariable_Wrap(made) : Py_NewRef(a[5]);
 }
 
-// No C++ exception leaves an entry: torch's allocator may throw.
+// No C++ exception leaves an entry: torch's allocator may throw, and Python
+// sees what it sees of torch's own calls (torch.OutOfMemoryError, ..).
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-    try {
-        return F(self, a, n);
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-    } catch (...) {
-        PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
-    }
-    return nullptr;
+    HANDLE_TH_ERRORS
+    return F(self, a, n);
+    END_HANDLE_TH_ERRORS
 }
 
 // bind(gdr_fwd, gdr_workspace_size, gdr_state_update, proj_q4): the entry points' addresses
