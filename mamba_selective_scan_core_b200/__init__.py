@@ -839,7 +839,7 @@ class _Torch:
         else:
             _calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 self.lib.mamba_gdr_fwd, self.lib.mamba_gdr_workspace_size, self.lib.mamba_gdr_state_update,
-                self.lib.mamba_proj_q4)))
+                self.lib.mamba_proj_q4)), MixerError)
             self.calls = _calls
 
 

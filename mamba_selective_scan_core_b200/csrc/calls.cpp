@@ -5,9 +5,10 @@
 // looked at where torch keeps them, the outputs come from torch's allocator,
 // and the C entry point is called by its address (of whichever build of the
 // library Python loaded).  A call that does not fit -- a tensor of another
-// type, shape, device or layout, an error status -- returns None without
-// having launched anything, and the Python side takes its own path, which
-// finds out what is wrong and says so.
+// type, shape, device or layout, an argument that the library refuses --
+// returns None without having launched anything, and the Python side takes its
+// own path, which finds out what is wrong and says so.  A launch that fails,
+// perhaps after others of the call, is raised here.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -30,6 +31,7 @@ struct Library {
     decltype(&mamba_gdr_workspace_size) gdr_workspace_size = nullptr;
     decltype(&mamba_gdr_state_update) gdr_state_update = nullptr;
     decltype(&mamba_proj_q4) proj_q4 = nullptr;
+    PyObject* error = nullptr;        // MixerError(status, name)
 } g_lib;
 
 // A tensor argument: null when it is None, `bad` when it is anything else
@@ -80,6 +82,14 @@ bool number(PyObject* o, float dflt, float& out) {
     return true;
 }
 PyObject* none() { Py_RETURN_NONE; }
+// what a status other than MM_OK makes of a call
+PyObject* failed(mm_status st, const char* name) {
+    if (st != MM_ERR_CUDA) return none();     // refused before its first launch
+    PyObject* e = PyObject_CallFunction(g_lib.error, "is", static_cast<int>(st), name);
+    if (e) PyErr_SetObject(g_lib.error, e);
+    Py_XDECREF(e);
+    return nullptr;
+}
 bool activation(at::ScalarType t) { return t == at::kBFloat16 || t == at::kFloat; }
 mm_dtype code(at::ScalarType t) { return t == at::kBFloat16 ? MM_BF16 : MM_F32; }
 
@@ -116,7 +126,7 @@ PyObject* gdr_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                        beta->const_data_ptr(), f32(bias), f32(A), f32(h0), y->mutable_data_ptr(),
                                        static_cast<float*>(h_last->mutable_data_ptr()), B, L, G, H, P, N, qs, ks, vs, scale, eps,
                                        code(type), ws->mutable_data_ptr(), ws->nbytes(), c10::cuda::getCurrentCUDAStream(dev).stream());
-    if (st != MM_OK) return none();
+    if (st != MM_OK) return failed(st, "mamba_gdr_fwd");
     PyObject* yo = y_new.defined() ? THPVariable_Wrap(y_new) : Py_NewRef(a[10]);
     PyObject* ho = h_new.defined() ? THPVariable_Wrap(h_new) : Py_NewRef(a[11]);
     PyObject* out = yo && ho ? PyTuple_Pack(2, yo, ho) : nullptr;
@@ -152,7 +162,7 @@ PyObject* gdr_state_update(PyObject*, PyObject* const* a, Py_ssize_t n) {
         q->const_data_ptr(), k->const_data_ptr(), v->const_data_ptr(), dt->const_data_ptr(), beta->const_data_ptr(), f32(bias), f32(A),
         static_cast<float*>(state->mutable_data_ptr()), y->mutable_data_ptr(), B, G, H, P, N, qs, ks, vs, scale, eps, code(type),
         c10::cuda::getCurrentCUDAStream(dev).stream());
-    if (st != MM_OK) return none();
+    if (st != MM_OK) return failed(st, "mamba_gdr_state_update");
     return y_new.defined() ? THPVariable_Wrap(y_new) : Py_NewRef(a[10]);
 }
 
@@ -181,7 +191,7 @@ PyObject* proj_q4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const mm_status st = g_lib.proj_q4(x->const_data_ptr(), W->const_data_ptr(), scales->const_data_ptr(),
                                        zeros ? zeros->const_data_ptr() : nullptr, out->mutable_data_ptr(), M, N, K, group, code(type),
                                        c10::cuda::getCurrentCUDAStream(dev).stream());
-    if (st != MM_OK) return none();
+    if (st != MM_OK) return failed(st, "mamba_proj_q4");
     return made.defined() ? THPVariable_Wrap(made) : Py_NewRef(a[5]);
 }
 
@@ -194,10 +204,10 @@ PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// bind(gdr_fwd, gdr_workspace_size, gdr_state_update, proj_q4): the entry points' addresses
+// bind(gdr_fwd, gdr_workspace_size, gdr_state_update, proj_q4, error): the entry points' addresses, and the class of a failure
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 4) {
-        PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
+    if (n != 5) {
+        PyErr_SetString(PyExc_TypeError, "bind takes four addresses and an exception class");
         return nullptr;
     }
     void* p[4];
@@ -209,6 +219,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g_lib.gdr_workspace_size = reinterpret_cast<decltype(g_lib.gdr_workspace_size)>(p[1]);
     g_lib.gdr_state_update = reinterpret_cast<decltype(g_lib.gdr_state_update)>(p[2]);
     g_lib.proj_q4 = reinterpret_cast<decltype(g_lib.proj_q4)>(p[3]);
+    Py_INCREF(a[4]);
+    Py_XSETREF(g_lib.error, a[4]);
     Py_RETURN_NONE;
 }
 
