@@ -53,16 +53,19 @@ bool dense(const at::Tensor* t, int dev, at::ScalarType type, at::IntArrayRef sh
 bool dense_or_none(const at::Tensor* t, int dev, at::ScalarType type, at::IntArrayRef shape) {
     return !t || dense(t, dev, type, shape);
 }
-// Elements between the rows of a [..., tokens, heads, width] tensor whose rows
-// are dense and evenly spaced; -1 when they are not.
+// Elements between the rows of a [.., heads, width] tensor (tokens, or
+// sequences and their tokens, before those) whose rows are dense and evenly
+// spaced; -1 when they are not.  A dimension of one has no stride to go by.
 int64_t row_stride(const at::Tensor* t, int dev, at::ScalarType type, at::IntArrayRef shape) {
     if (!t || !on(*t, dev, type) || t->sizes() != shape) return -1;
     const at::IntArrayRef st = t->strides();
     const size_t n = shape.size();
-    if (st[n - 1] != 1 || st[n - 2] != shape[n - 1]) return -1;
-    const int64_t rows = shape[n - 3];
-    if (n == 3) return rows > 1 ? st[0] : shape[1] * shape[2];
-    return rows > 1 && st[0] == rows * st[1] ? st[1] : -1;
+    if (st[n - 1] != 1 || (shape[n - 2] != 1 && st[n - 2] != shape[n - 1])) return -1;
+    const int64_t tokens = shape[n - 3], seqs = n == 4 ? shape[0] : 1;
+    if (tokens < 1) return -1;
+    if (seqs == 1) return tokens > 1 ? st[n - 3] : shape[n - 2] * shape[n - 1];
+    if (tokens == 1) return st[0];
+    return st[0] == tokens * st[1] ? st[1] : -1;
 }
 const float* f32(const at::Tensor* t) { return t ? static_cast<const float*>(t->const_data_ptr()) : nullptr; }
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {

@@ -54,3 +54,61 @@ def test_a_failed_launch_is_raised_at_once(monkeypatch):
             assert e.value.status == 7
         call()
     torch.cuda.synchronize()
+
+
+class Counting:
+    """names.calls, with how often each call gave a result."""
+
+    def __init__(self, calls):
+        self.calls, self.answered = calls, 0
+
+    def __getattr__(self, name):
+        call = getattr(self.calls, name)
+
+        def run(*args):
+            out = call(*args)
+            self.answered += out is not None
+            return out
+        return run
+
+
+def layouts(L):
+    """q, k, v of a call of L tokens in the layouts that programs have them in:
+    dense, parts of one packed tensor, a prompt cut from a longer buffer, one
+    key head."""
+    for B, G, packed in ((1, 2, False), (2, 2, True), (3, 1, True), (1, 1, False)):
+        yield to_cuda(gdr_inputs(B, L, G, 2, 64, 64, seed=L + B, packed=packed))
+    d = to_cuda(gdr_inputs(1, L + 5, 2, 2, 64, 64, seed=L, packed=True))
+    yield {k: t if k in ("A", "dt_bias", "h0") else t[:, :L] for k, t in d.items()}
+
+
+@pytest.mark.parametrize("L", [1, 2, 30, 200])
+def test_prefills_are_looked_at_in_c(monkeypatch, L):
+    names = mm._names()
+    counting = Counting(names.calls)
+    for n, d in enumerate(layouts(L)):
+        args = (d["q"], d["k"], d["v"], d["dt"], d["beta"], d["dt_bias"], d["A"], d["h0"])
+        monkeypatch.setattr(names, "calls", counting)
+        y, h = mm.gdr_fwd(*args)
+        assert counting.answered == n + 1, f"layout {n}: left to ctypes"
+        monkeypatch.setattr(names, "calls", None)
+        y2, h2 = mm.gdr_fwd(*args)
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(h, h2)
+
+
+def test_steps_and_projections_are_looked_at_in_c(monkeypatch):
+    counting = Counting(mm._names().calls)
+    monkeypatch.setattr(mm._names(), "calls", counting)
+    _, one, q4 = operands()
+    n = 0
+    for B in (1, 3):
+        d = to_cuda(gdr_inputs(B, None, 1, 2, 64, 64, F32, seed=5, packed=True))
+        mm.gdr_state_update(d["q"], d["k"], d["v"], d["dt"], d["beta"], d["dt_bias"], d["A"], d["h0"])
+        n += 1
+        assert counting.answered == n
+    for zeros, dtype in ((q4["zeros"], BF), (None, F32)):
+        mm.proj_q4(q4["x"], q4["W"], q4["scales"], zeros, group=64, out_dtype=dtype)
+        n += 1
+        assert counting.answered == n
+    torch.cuda.synchronize()
