@@ -831,17 +831,20 @@ class _Torch:
             (lambda i: torch.cuda.current_stream(i).cuda_stream)
         self.lib = lib()
         # the same calls with the tensors looked at in C++ (they return None
-        # where the Python below is to decide); without the module, this alone
-        try:
-            from . import _calls
-        except ImportError:
-            self.calls = None
-        else:
+        # where the Python below is to decide); without the module, or with one
+        # compiled against another torch or Python, this alone
+        from .build import calls_fit
+
+        self.calls = None
+        if calls_fit():
+            try:
+                from . import _calls
+            except ImportError:
+                return
             _calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 self.lib.mamba_gdr_fwd, self.lib.mamba_gdr_workspace_size, self.lib.mamba_gdr_state_update,
                 self.lib.mamba_proj_q4)), MixerError)
             self.calls = _calls
-
 
     def empty(self, like, shape, dtype, stream, given_back=True):
         """Memory for a call that runs on `stream`: torch's allocator hands out

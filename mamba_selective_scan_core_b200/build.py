@@ -60,11 +60,30 @@ def _compile(path: str, flags, verbose: bool) -> str:
     return path
 
 
+def calls_for() -> str:
+    """What the module of calls.cpp depends on besides its source: C++ of this
+    torch, C of this Python.  The module holds it as a string."""
+    import torch
+
+    return f"calls.cpp for torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def calls_fit() -> bool:
+    """Is there a module of calls.cpp compiled against what runs this?"""
+    try:
+        with open(CALLS_PATH, "rb") as f:
+            return calls_for().encode() + b"\0" in f.read()
+    except OSError:
+        return False
+
+
 def build_calls(force: bool = False, verbose: bool = False) -> str:
     """The module of calls.cpp, against the torch and Python that run this."""
     newest = max(os.path.getmtime(f) for f in (CALLS_SOURCE, os.path.join(INCLUDE, "mamba_mixer.h")))
-    if not force and os.path.exists(CALLS_PATH) and os.path.getmtime(CALLS_PATH) >= newest:
+    if not force and calls_fit() and os.path.getmtime(CALLS_PATH) >= newest:
         return CALLS_PATH
+    if os.path.exists(CALLS_PATH):
+        os.remove(CALLS_PATH)              # one that is behind its source is not loaded either
     import sysconfig
 
     import torch
@@ -72,7 +91,7 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = CALLS_PATH + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f'-DMM_CALLS_FOR="{calls_for()}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"),
            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
            CALLS_SOURCE, "-o", tmp, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
@@ -84,7 +103,11 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    build_calls(force, verbose)
+    try:
+        build_calls(force, verbose)
+    except (ImportError, OSError, RuntimeError, subprocess.CalledProcessError) as e:
+        # the library itself needs neither torch nor g++
+        print(f"{os.path.basename(CALLS_SOURCE)} is not compiled ({e}): its calls go through ctypes", file=sys.stderr)
     if not force and not stale(LIB_PATH):
         return LIB_PATH
     return _compile(LIB_PATH, list(extra_flags), verbose)

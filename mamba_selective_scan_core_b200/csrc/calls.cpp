@@ -233,7 +233,7 @@ PyMethodDef g_methods[] = {
     {"gdr_state_update", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<gdr_state_update>)), METH_FASTCALL, nullptr},
     {"proj_q4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<proj_q4>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
-PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", MM_CALLS_FOR, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
