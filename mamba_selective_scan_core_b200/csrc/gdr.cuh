@@ -10,9 +10,9 @@
 // normalises them.
 //
 // gdr_recurrent_kernel runs that as it stands for one token (decode),
-// gdr_tokens_kernel token by token: short calls and fp32 activations.  gdr_prep_kernel and
-// gdr_scan_kernel run longer bf16 calls in chunks of 64 tokens on the tensor
-// cores.
+// gdr_tokens_kernel four tokens at a time: short calls and fp32 activations.
+// gdr_prep_kernel and gdr_scan_kernel run longer bf16 calls in chunks of 64
+// tokens on the tensor cores.
 #pragma once
 
 #include <cstdint>
@@ -60,18 +60,23 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* gsrc, uint32_t 
                  :: "r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(bytes), "r"(smem_addr(bar)) : "memory");
 }
 
-// ---------------------------------------------------------------- token by token
-// State rows stay in registers for the whole call.  Eight lanes hold a row,
-// lane e its entries 4e + 32m + (0..3), so a warp's load of four rows is whole
-// 128-byte lines; a warp holds 4 RPT rows, a CTA of four warps 16 RPT.  Both
-// row sums of a token are taken of the state before it,
+// ---------------------------------------------------------------- one token
+// Eight lanes hold a state row, lane e its entries 4e + 32m + (0..3), so a
+// warp's load of four rows is whole 128-byte lines; a warp holds 4 RPT rows, a
+// CTA of four warps 16 RPT.  Both row sums of the token are taken of the state
+// before it,
 //     S_t q = a (S_{t-1} q) + b (v - a S_{t-1} k) (k . q),
-// so they are reduced together (three shuffles over the eight lanes) and the
-// update of the state is off the path from one sum to the next.
+// so they are reduced together (three shuffles over the eight lanes).  No token
+// (seqlen 0) copies the state.
+//
+// The state's traffic bounds it, for few rows a launch's latency: 128 sequences
+// of 64 heads (128 x 128) 159 us in bf16, 6.8 TB/s.  At N = 128 the compiler
+// gets the registers of three CTAs an SM: in those of four it has fewer of a
+// lane's loads in flight (166 us).
 constexpr int kGdrRecThreads = 128;
 
 template <typename T, int N, int RPT>
-__global__ void __launch_bounds__(kGdrRecThreads)
+__global__ void __launch_bounds__(kGdrRecThreads, N == 128 ? 3 : 1)
 gdr_recurrent_kernel(const GdrParams p)
 {
     constexpr int M = N / 32;                     // float4s of a row per lane
@@ -95,47 +100,21 @@ gdr_recurrent_kernel(const GdrParams p)
 
     const float bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
     const float A = p.A[h];
-    const int64_t t_first = static_cast<int64_t>(b) * p.L;
-    const T* kp = static_cast<const T*>(p.k) + t_first * p.k_stride + g * N + 4 * e;
-    const T* qp = static_cast<const T*>(p.q) + t_first * p.q_stride + g * N + 4 * e;
-    const T* vp = static_cast<const T*>(p.v) + t_first * p.v_stride + static_cast<int64_t>(h) * p.P + row0;
-    const T* dtp = static_cast<const T*>(p.dt) + t_first * p.H + h;
-    const T* bp = static_cast<const T*>(p.beta) + t_first * p.H + h;
-    T* yp = static_cast<T*>(p.y) + (t_first * p.H + h) * p.P + row0;
-
-    // the next token's inputs are loaded while the current one is worked on
-    float4 kn[M], qn[M];
-    float vn[RPT], dtn = 0.0f, bn = 0.0f;
-    auto fetch = [&]() {
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-            kn[m] = load4(kp + 32 * m);
-            qn[m] = load4(qp + 32 * m);
-        }
-#pragma unroll
-        for (int r = 0; r < RPT; ++r) vn[r] = Act<T>::load(vp + 4 * r);
-        dtn = Act<T>::load(dtp);
-        bn = Act<T>::load(bp);
-        kp += p.k_stride;
-        qp += p.q_stride;
-        vp += p.v_stride;
-        dtp += p.H;
-        bp += p.H;
-    };
-    if (p.L > 0) fetch();
-    for (int64_t t = 0; t < p.L; ++t) {
+    if (p.L > 0) {
+        const T* kp = static_cast<const T*>(p.k) + b * p.k_stride + g * N + 4 * e;
+        const T* qp = static_cast<const T*>(p.q) + b * p.q_stride + g * N + 4 * e;
+        const T* vp = static_cast<const T*>(p.v) + b * p.v_stride + static_cast<int64_t>(h) * p.P + row0;
+        const int64_t gate = static_cast<int64_t>(b) * p.H + h;
         float4 k[M], q[M];
         float v[RPT];
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            k[m] = kn[m];
-            q[m] = qn[m];
+            k[m] = load4(kp + 32 * m);
+            q[m] = load4(qp + 32 * m);
         }
 #pragma unroll
-        for (int r = 0; r < RPT; ++r) v[r] = vn[r];
-        const float a = expf(MathExact::step(dtn, bias) * A);
-        const float bt = 1.0f / (1.0f + expf(-bn));
-        if (t + 1 < p.L) fetch();
+        for (int r = 0; r < RPT; ++r) v[r] = Act<T>::load(vp + 4 * r);
+        const float dtn = Act<T>::load(static_cast<const T*>(p.dt) + gate), bn = Act<T>::load(static_cast<const T*>(p.beta) + gate);
 
         float kk = 0.0f, qq = 0.0f, kq = 0.0f;
 #pragma unroll
@@ -165,6 +144,8 @@ gdr_recurrent_kernel(const GdrParams p)
                 qs[r] += __shfl_xor_sync(kFull, qs[r], o);
             }
         }
+        const float a = expf(MathExact::step(dtn, bias) * A);
+        const float bt = 1.0f / (1.0f + expf(-bn));
         // the norms' factors go into the sums and the update instead of k and q
         const float rk = p.eps > 0.0f ? rsqrtf(kk + p.eps) : 1.0f;
         const float rq = (p.eps > 0.0f ? rsqrtf(qq + p.eps) : 1.0f) * p.scale;
@@ -184,8 +165,7 @@ gdr_recurrent_kernel(const GdrParams p)
                 s[r][m].w = fmaf(a, s[r][m].w, uk * k[m].w);
             }
         }
-        if (e < RPT) yp[4 * e] = Act<T>::from_f32(yv);
-        yp += static_cast<int64_t>(p.H) * p.P;
+        if (e < RPT) static_cast<T*>(p.y)[srow + 4 * e] = Act<T>::from_f32(yv);
     }
 #pragma unroll
     for (int r = 0; r < RPT; ++r)
@@ -194,7 +174,9 @@ gdr_recurrent_kernel(const GdrParams p)
             *reinterpret_cast<float4*>(p.h_last + (srow + 4 * r) * N + 4 * e + 32 * m) = s[r][m];
 }
 
-// The same for calls of several tokens.  What bounds those is the path from
+// ---------------------------------------------------------------- a few tokens at a time
+// The same for calls of several tokens, the state in the same lanes' registers
+// for the whole call.  What bounds those is the path from
 // one token's sums over the state to the next one's, so four tokens share it:
 // with c_i the product of the group's decays up to token i and D_ij that of
 // those after j,
