@@ -1992,13 +1992,20 @@ cudaError_t launch_gdr_one(const mm::GdrParams& p, int64_t batch, cudaStream_t s
     mm::gdr_recurrent_kernel<T, N, RPT><<<gdr_rows_grid<RPT>(p, batch), mm::kGdrRecThreads, forced_launch_failure() ? (1 << 20) : 0, s>>>(p);
     return cudaGetLastError();
 }
-// State rows per lane: more once the grid fills the SMs with them (fewer
-// reads of q and k per row), one below that (the latency of a row decides).
+// State rows a lane.  Several tokens: two where one would make more than one
+// CTA an SM (32 tokens of 2048 rows 7.7 us with one, 8.7 with two; of 2560 rows
+// 8.8 and 8.6; of 8192, 12.8 and 10.8, N = 128 20.4 and 14.5).  One token: four
+// from some CTAs an SM on (N = 64, 4096 rows 2.05 and 2.30 us with four, 9216
+// 2.69 and 2.56, 151552 18.2 and 14.7; N = 128 in bf16, 9216 rows 3.2 and 3.5,
+// 18944 6.3 and 5.9, 151552 29.1 and 27.0); N = 128 in fp32 one always (37888
+// rows 8.7 and 9.5, 151552 26.6 and 27.4).
 template <typename T, int N>
 cudaError_t launch_gdr_recurrent_n(const mm::GdrParams& p, int64_t batch, cudaStream_t s) {
-    const int64_t rows = batch * p.H * p.P / (mm::kGdrRecThreads / 8);        // CTAs of one row a lane
-    if (p.L > 1) return rows >= 16 * plan_sms() ? launch_gdr_tokens<T, N, 2>(p, batch, s) : launch_gdr_tokens<T, N, 1>(p, batch, s);
-    return rows >= 16 * plan_sms() ? launch_gdr_one<T, N, 4>(p, batch, s) : launch_gdr_one<T, N, 1>(p, batch, s);
+    const int64_t ctas = batch * p.H * p.P / (mm::kGdrRecThreads / 8), sms = plan_sms();      // of one row a lane
+    if (p.L > 1) return ctas > sms ? launch_gdr_tokens<T, N, 2>(p, batch, s) : launch_gdr_tokens<T, N, 1>(p, batch, s);
+    if constexpr (sizeof(T) == 2 || N == 64)
+        if (ctas >= (N == 64 ? 4 : 8) * sms) return launch_gdr_one<T, N, 4>(p, batch, s);
+    return launch_gdr_one<T, N, 1>(p, batch, s);
 }
 mm_status launch_gdr_recurrent(const mm::GdrParams& p, const GdrArgs& a, cudaStream_t s) {
     cudaError_t e;
