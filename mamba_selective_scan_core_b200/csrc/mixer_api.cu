@@ -2017,17 +2017,36 @@ mm_status launch_gdr_recurrent(const mm::GdrParams& p, const GdrArgs& a, cudaStr
     return e == cudaSuccess ? MM_OK : MM_ERR_CUDA;
 }
 
-// The chunked form: bf16 calls of enough tokens.  One chunk costs 13 us (two
-// dependent kernels, the triangular system between them); token by token, a
-// block of 8 tokens costs 1.3 to 2.2 us while the state's rows leave the SMs
-// free (crossing at 41 to 62 tokens), 14 us with 32768 rows of 128 (at 11).
+// Whether a bf16 call runs in chunks: every one of more than two chunks, a
+// shorter one where this model of both forms' times, in us, says so.
+//
+// Four tokens at a time, a call takes a latency a block of 8 tokens as long as
+// an SM has few state rows, and the rows' time above that.  In chunks, the
+// scan's waves of 64-row tiles, one a SM, each with its start and its chunks,
+// after the chunks' systems.  Fitted to both forms' times at 8 to 128 tokens of
+// 128 to 262144 rows, 30 sizes x 12 lengths; where it takes the slower one,
+// that is at most 7% slower.  They cross at 81 tokens (N = 64) and 73 (N = 128)
+// for 128 rows, 49 and 33 for 8192, 33 and 25 for 16384, 33 and 17 for 65536 of
+// 512 heads, 41 and 25 for as many of 1024.  128 rows of N = 64: 48 tokens 9.8
+// us (14.9 in chunks), 128 tokens 21.5 (18.2); 16384 rows, 24 tokens 16.4
+// (21.1), 64 tokens 35.2 (21.5); 65536 rows of 1024 heads, 16 tokens 33.8
+// (73.1), 64 tokens 106 (78).
+bool gdr_in_chunks(int64_t batch, int64_t seqlen, int64_t heads, int64_t headdim, int64_t d_state, int64_t sms) {
+    const int64_t chunks = (seqlen + mm::kGdrC - 1) / mm::kGdrC, blocks = (seqlen + mm::kGdrBlock - 1) / mm::kGdrBlock;
+    const int64_t tiles = batch * heads * headdim / mm::kGdrTile, waves = (tiles + sms - 1) / sms;
+    if (chunks > 2) return true;
+    const bool wide = d_state == 128;
+    const double an_sm = 1.0 / static_cast<double>(sms), rows = static_cast<double>(batch * heads * headdim) * an_sm;
+    const double row = rows < 256 ? (wide ? 0.061 : 0.034) : (wide ? 0.053 : 0.027);
+    const double tokens = 2.2 + std::max(wide ? 1.5 : 1.22, rows * row) * static_cast<double>(blocks);
+    const double scan = static_cast<double>(waves) * ((wide ? 5.6 : 2.5) + (wide ? 2.1 : 2.8) * static_cast<double>(chunks));
+    return 6.8 + scan + 3.4 * an_sm * static_cast<double>(batch * heads * chunks) < tokens;
+}
 // The workspace is kept to kGdrRoundUnits chunks of a head (of a sequence's
 // heads, where it has more): the sequences go in parts, one after another, and
 // a part's chunks in rounds of as many as that allows, each round from the
 // state that the one before left in the workspace (two of them in turn: a
 // round's first segment reads one while its last writes the other).
-constexpr int64_t kGdrManyRows = 16384;        // state rows of all heads
-int64_t gdr_chunked_min(int64_t rows) { return rows >= kGdrManyRows ? 16 : 44; }
 constexpr int64_t kGdrRoundUnits = 16384;      // 50 KB each
 struct GdrPlan {
     bool chunked = false;
@@ -2059,7 +2078,7 @@ int gdr_segments(int64_t batch, int64_t tiles, int64_t trans_tiles, int64_t chun
 }
 GdrPlan plan_gdr(int64_t batch, int64_t seqlen, int64_t heads, int64_t headdim, int64_t d_state, mm_dtype act, int64_t sms) {
     GdrPlan pl;
-    if (act != MM_BF16 || seqlen < gdr_chunked_min(batch * heads * headdim)) return pl;
+    if (act != MM_BF16 || seqlen < 2 || !gdr_in_chunks(batch, seqlen, heads, headdim, d_state, sms)) return pl;
     pl.chunked = true;
     const int64_t most = std::max<int64_t>(1, kGdrRoundUnits / heads), parts = (batch + most - 1) / most;
     pl.part = (batch + parts - 1) / parts;

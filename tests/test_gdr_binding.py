@@ -103,3 +103,16 @@ def test_workspace_is_bounded(B, L, H, P, N):
     bound = 256 + units * (5 * 64 * 4 + 6 * 64 * 128) + 2 * units * P * N * 4 + 32 * 256 * (2 * P + N) * N * 4
     assert 256 < mm.gdr_workspace_size(B, L, H, P, N, 1) <= bound
     assert mm.gdr_workspace_size(B, L, H, P, N, 1) <= mm.gdr_workspace_size(B, 4 * L, H, P, N, 1)
+
+
+@pytest.mark.parametrize("B,L,H,P,N,chunks", [
+    (1, 48, 2, 64, 64, False), (1, 64, 16, 128, 64, False), (1, 24, 32, 128, 128, False), (32, 16, 32, 64, 64, False),
+    (16, 16, 64, 128, 64, False), (64, 16, 64, 64, 64, False), (32, 16, 32, 64, 128, False),
+    (1, 128, 2, 64, 64, True), (1, 128, 16, 128, 128, True), (4, 48, 32, 128, 64, True), (4, 32, 32, 128, 128, True),
+    (8, 48, 64, 128, 64, True), (16, 48, 64, 128, 128, True), (64, 64, 64, 64, 128, True), (1, 129, 1, 64, 64, True)])
+def test_which_calls_run_in_chunks(B, L, H, P, N, chunks):
+    """Sizes at which the other form took 1.25 to 2.2 times as long; a call that
+    is not in chunks has no workspace but its status."""
+    mmbuild.build()
+    assert (mm.gdr_workspace_size(B, L, H, P, N, 1) > 256) == chunks
+    assert mm.gdr_workspace_size(B, L, H, P, N, 1, act=mm.MM_F32) == 256

@@ -10,7 +10,7 @@ from gdr_ref import BF
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("B,L,H,given", [(600, 70, 64, True), (260, 200, 65, False)])
+@pytest.mark.parametrize("B,L,H,given", [(600, 140, 64, True), (260, 200, 65, False)])
 def test_many_sequences(B, L, H, given):
     P, N = 64, 64
     g = torch.Generator(device="cuda").manual_seed(B)
