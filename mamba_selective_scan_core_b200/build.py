@@ -1,8 +1,9 @@
 """Compile the CUDA library (sm_100a) in-tree: libmamba_mixer.so next to this
 file, and its checked build libmamba_mixer_checked.so (compiled with
 MM_CHECK_BOUNDS: the forward and decode kernels check every index they form
-against its buffer, skip an access outside it and report MM_ERR_BOUNDS); and
-the Python module of the calls a decoded token makes, _calls.so.
+against its buffer, skip an access outside it and report MM_ERR_BOUNDS; those of
+the gated delta rule and of the 4-bit projection do not); and the Python module
+of the calls a decoded token makes, _calls.so, where that can be compiled.
 
     python -m mamba_selective_scan_core_b200.build [--force] [--verbose] [--checked]
 """

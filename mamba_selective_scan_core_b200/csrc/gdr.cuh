@@ -191,7 +191,8 @@ gdr_recurrent_kernel(const GdrParams p)
 // copies a block; a copy a row takes 90 cycles each to issue) two blocks ahead,
 // beside the four warps that hold the state.  All in fp32.  2 x 200 fp32 tokens
 // of 16 heads (128 x 64): 90 us with the next token's loads in registers, 68
-// a token at a time with a ring that all warps fill, 41 this way.
+// a token at a time with a ring that all warps fill, 40 this way, 34 with two
+// rows a lane.
 constexpr int kGdrBlock = 8;          // tokens of a ring slot: two groups
 constexpr int kGdrGroup = 4;
 constexpr int kGdrTokThreads = kGdrRecThreads + 64;
@@ -497,13 +498,15 @@ gdr_tokens_kernel(const GdrParams p, const __grid_constant__ CUtensorMap tm_q, c
 //
 // What bounds them.  The prep kernel: the phases of a chunk's system, most of
 // which keep two to four of its eight warps busy (warps wait at barriers 40% of
-// their time; 0.46 instructions a cycle and scheduler): 24 ns a chunk of a head
+// their time; 0.46 instructions a cycle and scheduler): 28 ns a chunk of a head
 // with four blocks an SM, 10 us for one alone.  The scan: its chain of three
-// products a chunk, 3.1 us, of which about 1500 cycles are the products', 2000
-// the elementwise work on two of the four schedulers (tensor-memory lanes
-// 0..63, the keys' rows, belong to those), the rest waits and hand-overs; the
-// tensor pipe is busy 26% of the time.  Longer chunks need more shared memory
-// than there is for [T; M T].
+// products a chunk, 3.8 us (N = 128).  With stamps of the clock in it a chunk
+// takes 7060 cycles: 2060 are the products' (8 steps of 96 cycles, 4 of 209, 4
+// of 113; the tensor pipe is busy 28% of the time), 3260 elementwise (S's parts
+// 990, X 1040, u' 1020, the state 210; X and u' on two of the four schedulers,
+// which tensor-memory lanes 0..63, the keys' rows, belong to), 1740 go between
+// them: barriers, reads of tensor memory, warps that end after one another.
+// Longer chunks need more shared memory than there is for [T; M T].
 //
 // The decays' exponents are differences of the prefix sums, which are taken
 // in fp64 and kept as two floats: the sums reach hundreds, the differences of
@@ -513,8 +516,8 @@ gdr_tokens_kernel(const GdrParams p, const __grid_constant__ CUtensorMap tm_q, c
 // A product takes whole rows, zeros of T and M among them, and 0 x NaN would
 // carry a token that is not finite to those before it.  So the kernels keep
 // such values out of T and X (0 in their place), remember the first token from
-// which a channel is not finite, and put NaN into its u' and y from there on (12 us of
-// 356).
+// which a channel is not finite, and put NaN into its u' and y from there on
+// (12 us of 356, 4096 tokens x 64 heads).
 constexpr int kGdrC = 64;             // tokens per chunk
 constexpr int kGdrTile = 64;          // state rows per CTA of the scan
 constexpr int kGdrFac = 5 * kGdrC;    // factors of a chunk

@@ -25,11 +25,15 @@
 // s (8 - z) sum_k x[m, k], whose sum is one more mma with a matrix of ones; an
 // output that is not finite is worked out again term by term.
 //
-// What bounds it: the integer pipe.  A product's 16 x 128 weights take 32
-// mask-and-ors, 24 shifts and 16 byte permutes there, at two cycles each; in
-// 16384 x 16384 with one row, 52 us, the copies alone take 29 us, the rest alone
-// 47 (38 without the shifts, 44 without the subtractions or the permutes).
-// 16384 x 4096, one row: 15.2 us, 2.3 TB/s.
+// What bounds it: the instructions around the products.  For 16384 x 16384 with
+// one row (52 us) 240 are executed for a warp's 16 x 128 weights, 126 of them
+// on the integer pipe at two cycles each: 252 of the 390 cycles that these
+// weights have on a scheduler of the SMs with two blocks (of 256 blocks on 148
+// SMs; over all, 0.61 instructions a cycle).  Unpacking is 72 of the 126 (32
+// mask-and-ors, 24 shifts, 16 byte permutes of x); what the others are has not
+// been taken apart.  The copies alone take 29 us, the rest alone 47 (38 without
+// the shifts, 44 without the subtractions or the permutes).  16384 x 4096, one
+// row: 15.8 us, 2.2 TB/s.
 //
 // Unpacking: (w >> 4i) & 0x000f000f | 0x43004300 is the bf16 pair
 // (128 + c_i, 128 + c_{i+4}) of a word of eight; one packed subtraction of 136
